@@ -234,7 +234,8 @@ def encode(x, bits):
     top = float(2 ** bits - 1)
     y = x.reshape(*x.shape[:-1], -1, GROUP)
     lo, hi = y.amin(-1, keepdim=True) + 0.0, y.amax(-1, keepdim=True) + 0.0
-    s16, z16 = ((hi - lo) / top).half(), lo.half()
+    # by a tensor: torch divides by a number as a product with its reciprocal, which rounds otherwise
+    s16, z16 = ((hi - lo) / torch.full_like(hi, top)).half(), lo.half()
     s, z = s16.float(), z16.float()
     codes = torch.where(s == 0, 0.0, ((y - z) / torch.where(s == 0, 1.0, s)).round().clamp(0, top)).to(torch.uint8)
     per = 8 // bits
