@@ -20,7 +20,7 @@ Format and method, by source page:
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -103,8 +103,12 @@ class Q4KVPool:
         self.mask = torch.zeros((n_q4_blocks + n_q8_blocks + n_q2_blocks, 8), dtype=torch.int32,
                                 device=self.device)
         self.error_word = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._describe()
+
+    def _describe(self) -> None:
+        n_q4_blocks, n_q8_blocks, n_q2_blocks = self.n_q4_blocks, self.n_q8_blocks, self.n_q2_blocks
         self.desc = _lib.PoolDesc(
-            head_dim, n_kv_heads, int(self.k_rotated), n_q4_blocks, n_q8_blocks, int(self.fp8),
+            self.head_dim, self.n_kv_heads, int(self.k_rotated), n_q4_blocks, n_q8_blocks, int(self.fp8),
             self.k_codes4.data_ptr(), self.v_codes4.data_ptr(),
             self.k_params4.data_ptr(), self.v_params4.data_ptr(),
             self.k_codes8.data_ptr() if n_q8_blocks else 0,
@@ -117,6 +121,48 @@ class Q4KVPool:
             self.v_codes2.data_ptr() if n_q2_blocks else 0,
             self.k_params2.data_ptr() if n_q2_blocks else 0,
             self.v_params2.data_ptr() if n_q2_blocks else 0)
+
+    @classmethod
+    def from_tensors(cls, n_kv_heads: int, head_dim: int, mask: torch.Tensor, k_rotated: bool = True,
+                     fp8: bool = False, error_word: Optional[torch.Tensor] = None,
+                     **arrays: torch.Tensor) -> "Q4KVPool":
+        """A pool over arrays the caller owns (contiguous, shaped and typed as
+        the class describes; block classes left out have no blocks).  The pool
+        keeps references; nothing is copied."""
+        widths = {"4": head_dim // 2, "8": head_dim, "2": head_dim // 4}
+        self = cls.__new__(cls)
+        self.device = _require_cuda(mask, *arrays.values())
+        self.fp8, self.k_rotated = bool(fp8), bool(k_rotated)
+        self.n_kv_heads, self.head_dim = n_kv_heads, head_dim
+        known = {f"{x}_{part}{w}" for x in "kv" for part in ("codes", "params") for w in widths}
+        if set(arrays) - known:
+            raise ValueError(f"unknown pool arrays {sorted(set(arrays) - known)}")
+        counts = {}
+        for w, row in widths.items():
+            n = counts[w] = arrays[f"k_codes{w}"].shape[0] if f"k_codes{w}" in arrays else 0
+            n_par = 0 if fp8 else n                              # FP8 blocks carry no params
+            shapes = {"codes": ((n, n_kv_heads, BLOCK_TOKENS, row), torch.uint8),
+                      "params": ((n_par, n_kv_heads, BLOCK_TOKENS, head_dim // GROUP, 2), torch.float16)}
+            for x in "kv":
+                for part, (shape, dtype) in shapes.items():
+                    t = arrays.get(f"{x}_{part}{w}")
+                    if t is None and shape[0] == 0:
+                        t = torch.empty(shape, dtype=dtype, device=self.device)
+                    if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                        raise ValueError(f"{x}_{part}{w} must be contiguous {dtype} of shape {shape}")
+                    setattr(self, f"{x}_{part}{w}", t)
+        self.n_q4_blocks, self.n_q8_blocks, self.n_q2_blocks = counts["4"], counts["8"], counts["2"]
+        if fp8 and (self.n_q4_blocks or self.n_q2_blocks or k_rotated):
+            raise ValueError("an FP8 pool has only 8-bit blocks and raw keys (k_rotated = False)")
+        if tuple(mask.shape) != (self.n_blocks, 8) or mask.dtype != torch.int32 or not mask.is_contiguous():
+            raise ValueError(f"mask must be contiguous int32 of shape {(self.n_blocks, 8)}")
+        if error_word is None:
+            error_word = torch.zeros(4, dtype=torch.int32, device=self.device)
+        elif error_word.device != self.device or error_word.dtype != torch.int32 or error_word.numel() < 1:
+            raise ValueError("error_word must be int32 on the pool's device")
+        self.mask, self.error_word = mask, error_word
+        self._describe()
+        return self
 
     @property
     def n_blocks(self) -> int:
@@ -173,6 +219,51 @@ class Q4KVPool:
                                        k.stride(0), k.stride(1), _ptr(tab), tab.shape[1], _ptr(lens),
                                        _stream(dev)),
               "q4kv_append_tokens")
+
+    def append_rotary(self, k: torch.Tensor, v: torch.Tensor, rotary: "Rotary", tables: torch.Tensor,
+                      seq_lens: torch.Tensor, n_new: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                      q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+        """Rotate new tokens' keys k [B][T][Hkv][D] by their positions and
+        write them with v as `append` does, in one launch; queries
+        q [B][T][Hq][D] are rotated along and returned (rows at or past
+        n_new[b] are 0).  positions is [n_axes][B][T]; None places token i of
+        sequence b at seq_lens[b] + i on every axis.  q_out may be q."""
+        dev = _require_cuda(self.mask, k, v, tables, seq_lens, n_new, positions, q, q_out, rotary.table)
+        _check_chunk(k, "k")
+        _check_chunk(v, "v")
+        if k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v must share dtype, shape and strides")
+        B, T, hkv, d = k.shape
+        if (hkv, d) != (self.n_kv_heads, self.head_dim):
+            raise ValueError(f"k and v must have {self.n_kv_heads} heads of {self.head_dim}")
+        tab, lens, nn = _sequences(B, tables, seq_lens, n_new)
+        pos = None
+        if positions is not None:
+            if tuple(positions.shape) != (rotary.desc.n_axes, B, T):
+                raise ValueError(f"positions must be [{rotary.desc.n_axes}][B][T]")
+            pos = positions.to(torch.int32).contiguous()
+        hq, qs, os_ = 0, (0, 0), (0, 0)
+        if q is not None:
+            _check_chunk(q, "q")
+            hq = q.shape[2]
+            if q.dtype != k.dtype or tuple(q.shape) != (B, T, hq, d):
+                raise ValueError("q must be [B][T][Hq][D] of the keys' dtype")
+            if q_out is None:
+                q_out = torch.empty((B, T, hq, d), dtype=q.dtype, device=dev)
+            _check_chunk(q_out, "q_out")
+            if q_out.shape != q.shape or q_out.dtype != q.dtype:
+                raise ValueError("q_out must have q's shape and dtype")
+            qs, os_ = _row_strides(q), _row_strides(q_out)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        ks = _row_strides(k)
+        with torch.cuda.device(dev):
+            check(lib().q4kv_append_rotary(
+                ctypes.byref(self.desc), ctypes.byref(rotary.desc), _ptr(k), _ptr(v), _IN_DTYPES[k.dtype], B, T, _ptr(nn),
+                ks[0], ks[1], _ptr(q), hq, qs[0], qs[1], _ptr(q_out), os_[0], os_[1], _ptr(tab), tab.shape[1],
+                _ptr(lens), _ptr(pos), _stream(dev)), "q4kv_append_rotary")
+        return q_out
 
     def invalidate(self, slot_ids: torch.Tensor) -> None:
         """Remap physical slots (block * 256 + offset) to the sentinel."""
@@ -244,6 +335,39 @@ class Q4KVPool:
               "q4kv_dequantize")
         return k, v
 
+    def gather(self, tables: torch.Tensor, starts: Optional[torch.Tensor], offsets: torch.Tensor, n_rows: int,
+               out_dtype=torch.float16, unrotate_k: bool = False, k_out: Optional[torch.Tensor] = None,
+               v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """K_hat, V_hat [n_rows][Hkv][D] of token ranges, packed: rows
+        offsets[b] .. offsets[b+1]-1 are the tokens of sequence b from
+        starts[b] (None = 0) on, found through tables [B][max_blocks].  Rows
+        that no sequence covers are left as they were (undefined where this
+        call allocates the outputs).  Remapped slots read K = -1e4, V = 0."""
+        dev = _require_cuda(self.mask, tables, starts, offsets, k_out, v_out)
+        B = tables.shape[0]
+        if tables.dim() != 2 or tuple(offsets.shape) != (B + 1,) or (starts is not None and tuple(starts.shape) != (B,)):
+            raise ValueError("tables must be [B][max_blocks], offsets [B+1] and starts [B]")
+        if out_dtype not in _OUT_DTYPES:
+            raise ValueError("out_dtype must be float32, float16 or bfloat16")
+        shape = (int(n_rows), self.n_kv_heads, self.head_dim)
+        outs = []
+        for o, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if o is None:
+                o = torch.empty(shape, dtype=out_dtype, device=dev)
+            elif tuple(o.shape) != shape or o.dtype != out_dtype or o.stride(2) != 1 or o.stride(1) != shape[2]:
+                raise ValueError(f"{name} must be {out_dtype} of shape {shape} with contiguous rows")
+            outs.append(o)
+        if shape[0] > 1 and outs[0].stride(0) != outs[1].stride(0):
+            raise ValueError("k_out and v_out must have equal strides")
+        stride = outs[0].stride(0) if shape[0] > 1 else shape[1] * shape[2]
+        tab, off = tables.to(torch.int32).contiguous(), offsets.to(torch.int32).contiguous()
+        st = None if starts is None else starts.to(torch.int32).contiguous()
+        with torch.cuda.device(dev):
+            check(lib().q4kv_gather_tokens(ctypes.byref(self.desc), _ptr(tab), tab.shape[1], B, _ptr(st), _ptr(off),
+                                           shape[0], _ptr(outs[0]), _ptr(outs[1]), stride, _OUT_DTYPES[out_dtype],
+                                           int(unrotate_k), _stream(dev)), "q4kv_gather_tokens")
+        return outs[0], outs[1]
+
     def read_device_error(self, clear: bool = True) -> int:
         """Synchronise the current stream and return the device error bits."""
         bits = ctypes.c_uint32(0)
@@ -252,6 +376,61 @@ class Q4KVPool:
         if st not in (_lib.OK, _lib.ERR_DEVICE):
             check(st, "q4kv_read_device_error")
         return int(bits.value)
+
+
+def _check_chunk(x: torch.Tensor, name: str) -> None:
+    if x.dtype not in _IN_DTYPES or x.dim() != 4:
+        raise ValueError(f"{name} must be float16 or bfloat16 [B][T][H][D]")
+    if x.stride(3) != 1 or x.stride(2) != x.shape[3]:
+        raise ValueError(f"each token's [H][D] row of {name} must be contiguous")
+
+
+def _row_strides(x: torch.Tensor) -> Tuple[int, int]:
+    """Sequence and token stride in elements; an axis of one entry has no stride of its own."""
+    row = x.shape[2] * x.shape[3]
+    token = x.stride(1) if x.shape[1] > 1 else row
+    return (x.stride(0) if x.shape[0] > 1 else token * max(x.shape[1], 1)), token
+
+
+def _sequences(B: int, tables: torch.Tensor, seq_lens: torch.Tensor, n_new: Optional[torch.Tensor]):
+    if tables.dim() != 2 or tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("tables must be [B][max_blocks] and seq_lens [B]")
+    if n_new is not None and tuple(n_new.shape) != (B,):
+        raise ValueError("n_new must be [B]")
+    return (tables.to(torch.int32).contiguous(), seq_lens.to(torch.int32).contiguous(),
+            None if n_new is None else n_new.to(torch.int32).contiguous())
+
+
+class Rotary:
+    """Rotary positions of a model: the (cos, sin) table and the axis of each pair.
+
+    table: float32 CUDA tensor [max_positions][rot_dim/2][2], the (cos, sin) of
+    pair f at position p.  Pairs are channels (f, f + rot_dim/2), or (2f, 2f+1)
+    when interleaved.  axis_of_pair gives each pair's position axis (time,
+    height, width, ...); None puts every pair on one axis.  n_axes defaults to
+    the largest axis named plus one."""
+
+    def __init__(self, table: torch.Tensor, axis_of_pair: Optional[Sequence[int]] = None, interleaved: bool = False,
+                 n_axes: Optional[int] = None):
+        _require_cuda(table)
+        if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+            raise ValueError("table must be contiguous float32 [max_positions][rot_dim/2][2]")
+        pairs = table.shape[1]
+        axis = [0] * pairs if axis_of_pair is None else [int(a) for a in axis_of_pair]
+        n_axes = max(axis, default=0) + 1 if n_axes is None else int(n_axes)
+        if pairs < 16 or pairs % 16 or pairs > _lib.MAX_PAIRS or len(axis) != pairs:
+            raise ValueError(f"rot_dim must be a multiple of 32 up to {2 * _lib.MAX_PAIRS}, with one axis per pair")
+        if not 1 <= n_axes <= _lib.MAX_AXES or min(axis) < 0 or max(axis) >= n_axes:
+            raise ValueError(f"axes must lie in [0, n_axes) with at most {_lib.MAX_AXES} axes")
+        self.table = table
+        self.desc = _lib.RotaryDesc(2 * pairs, int(interleaved), n_axes, table.shape[0], table.data_ptr(),
+                                    (ctypes.c_uint8 * _lib.MAX_PAIRS)(*axis))
+
+    @staticmethod
+    def make_table(inv_freq: torch.Tensor, max_positions: int, device="cuda") -> torch.Tensor:
+        """(cos, sin) of p * inv_freq[f], angles and functions in 64 bits, rounded once to float32."""
+        angle = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv_freq.to(device, torch.float64)
+        return torch.stack((angle.cos(), angle.sin()), -1).float().contiguous()
 
 
 def card_max_bytes(head_dim: int, n_kv_heads: int, n_tokens: int) -> int:
@@ -423,5 +602,57 @@ def append_decode(pool: Q4KVPool, k_new: torch.Tensor, v_new: torch.Tensor, q: t
     return out
 
 
+class ExtendPlan:
+    """Launch plan for the attention of one chunk shape (split count, workspace size)."""
+
+    def __init__(self, batch: int, max_new: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                 max_blocks_per_seq: int, window: int = 0, n_splits: int = 0, num_sms: int = 0):
+        self.c = _lib.ExtendPlan()
+        check(lib().q4kv_extend_plan_make(batch, max_new, n_q_heads, n_kv_heads, head_dim, max_blocks_per_seq, window,
+                                          n_splits, num_sms, ctypes.byref(self.c)), "q4kv_extend_plan_make")
+
+    def __getattr__(self, name):
+        return getattr(self.__dict__["c"], name)
+
+    def workspace(self, device) -> Optional[torch.Tensor]:
+        n = self.c.workspace_bytes
+        return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def extend_attention(pool: Q4KVPool, q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     n_new: Optional[torch.Tensor] = None, softmax_scale: float = 0.0, window: int = 0,
+                     out_dtype=torch.float16, plan: Optional[ExtendPlan] = None,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """GQA attention of each sequence's new tokens q [B][T][Hq][D] over its
+    cache, which already holds them (append or append_rotary ran before).
+
+    seq_lens holds the lengths before the new tokens: token i < n_new[b] (all T
+    when n_new is None) sees positions t <= seq_lens[b] + i and, with window >
+    0, t > seq_lens[b] + i - window.  Rows at or past n_new[b] are 0."""
+    dev = _require_cuda(pool.mask, q, block_tables, seq_lens, n_new, workspace, out)
+    _check_chunk(q, "q")
+    B, T, hq, d = q.shape
+    tab, lens, nn = _sequences(B, block_tables, seq_lens, n_new)
+    with torch.cuda.device(dev):
+        if plan is None:
+            plan = ExtendPlan(B, T, hq, pool.n_kv_heads, d, tab.shape[1], window=window)
+        elif (plan.batch, plan.max_new, plan.n_q_heads, plan.max_blocks_per_seq, plan.window) != \
+                (B, T, hq, tab.shape[1], window):
+            raise ValueError("the plan was made for another batch, chunk, head count, table width or window")
+        if workspace is None:
+            workspace = plan.workspace(dev)
+        if out is None:
+            out = torch.empty((B, T, hq, d), dtype=out_dtype, device=dev)
+        elif out.shape != q.shape or out.dtype not in _OUT_DTYPES or out.stride(3) != 1 or out.stride(2) != d:
+            raise ValueError("out must be [B][T][Hq][D] with contiguous rows")
+        qs, os_ = _row_strides(q), _row_strides(out)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        check(lib().q4kv_extend_attention(ctypes.byref(pool.desc), ctypes.byref(plan.c), _ptr(q), _IN_DTYPES[q.dtype],
+                                          qs[0], qs[1], _ptr(tab), _ptr(lens), _ptr(nn), float(softmax_scale),
+                                          _ptr(out), _OUT_DTYPES[out.dtype], os_[0], os_[1], _ptr(workspace),
+                                          ws_bytes, _stream(dev)), "q4kv_extend_attention")
+    return out
+
+
 __all__ = ["Q4KVPool", "Q4KVError", "DecodePlan", "decode_attention", "append_decode", "block_absmean",
-           "mixed_block_ids", "card_max_bytes", "card_encode", "card_decode", "BLOCK_TOKENS", "GROUP"]
+           "mixed_block_ids", "Rotary", "ExtendPlan", "extend_attention", "card_max_bytes", "card_encode", "card_decode", "BLOCK_TOKENS", "GROUP"]

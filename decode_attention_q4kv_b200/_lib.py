@@ -1,4 +1,5 @@
-"""ctypes view of libq4kv.so: structs and signatures of include/q4kv.h.
+"""ctypes view of libq4kv.so: structs and signatures of include/q4kv.h and
+include/q4kv_extend.h.
 
 Loading never falls back to anything: if the library cannot be built or
 loaded, the error propagates.
@@ -16,10 +17,13 @@ c_int32, c_int64, c_size_t, c_void_p, c_float = (ctypes.c_int32, ctypes.c_int64,
                                                   ctypes.c_void_p, ctypes.c_float)
 
 HEADER = os.path.join(_build.INCLUDE, "q4kv.h")
+EXTEND_HEADER = os.path.join(_build.INCLUDE, "q4kv_extend.h")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_DEVICE = range(6)
 F16, BF16, F32 = 0, 1, 2
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT_ID, DEVERR_TIMEOUT, DEVERR_IMAGE, DEVERR_WIDTH = 1, 2, 4, 8, 16, 32
+DEVERR_POSITION = 64
+MAX_AXES, MAX_PAIRS = 4, 128
 
 
 class PoolDesc(ctypes.Structure):
@@ -39,6 +43,17 @@ class DecodePlan(ctypes.Structure):
     _fields_ = [("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
                 ("head_dim", c_int32), ("max_blocks_per_seq", c_int32), ("n_splits", c_int32),
                 ("tokens_per_split", c_int32), ("kernel", c_int32), ("workspace_bytes", c_size_t)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int32), ("interleaved", c_int32), ("n_axes", c_int32), ("max_positions", c_int32),
+                ("table", c_void_p), ("axis", ctypes.c_uint8 * MAX_PAIRS)]
+
+
+class ExtendPlan(ctypes.Structure):
+    _fields_ = [("batch", c_int32), ("max_new", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("max_blocks_per_seq", c_int32), ("window", c_int32), ("n_splits", c_int32),
+                ("decode_splits", c_int32), ("reserved", c_int32), ("workspace_bytes", c_size_t)]
 
 
 P = ctypes.POINTER
@@ -82,13 +97,26 @@ _SIGNATURES = {
                                                        c_int32, c_void_p]),
 }
 
+_EXTEND_SIGNATURES = {
+    "q4kv_append_rotary": (c_int32, [P(PoolDesc), P(RotaryDesc), c_void_p, c_void_p, c_int32, c_int32, c_int32,
+                                     c_void_p, c_int64, c_int64, c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                     c_int64, c_int64, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
+    "q4kv_gather_tokens": (c_int32, [P(PoolDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p,
+                                     c_void_p, c_int64, c_int32, c_int32, c_void_p]),
+    "q4kv_extend_plan_make": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                        c_int32, P(ExtendPlan)]),
+    "q4kv_extend_attention": (c_int32, [P(PoolDesc), P(ExtendPlan), c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                        c_void_p, c_void_p, c_float, c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                        c_size_t, c_void_p]),
+}
+
 _lib = None
 _lock = threading.Lock()
 
 
-def header_functions():
-    """Names of the functions include/q4kv.h declares."""
-    text = open(HEADER).read()
+def header_functions(header: str = HEADER):
+    """Names of the functions a header (include/q4kv.h by default) declares."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(q4kv_\w+)\s*\(", text)))
 
@@ -100,7 +128,7 @@ def lib() -> ctypes.CDLL:
         if _lib is None:
             path = _build.build()
             dll = ctypes.CDLL(path)
-            for name, (res, args) in _SIGNATURES.items():
+            for name, (res, args) in {**_SIGNATURES, **_EXTEND_SIGNATURES}.items():
                 fn = getattr(dll, name)
                 fn.restype = res
                 fn.argtypes = args

@@ -1,0 +1,238 @@
+// Host side of include/q4kv_extend.h: argument checks, launch plans and
+// dispatch.  Every check happens before anything is enqueued.
+#include <math.h>
+#include <string.h>
+
+#include "extend_internal.cuh"
+
+using namespace q4kv;
+
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+inline q4kv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? Q4KV_OK : Q4KV_ERR_CUDA; }
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// A [batch][max_new] array of rows of `row` elements of `size` bytes.
+bool rows_ok(const void* p, int64_t seq_stride, int64_t token_stride, int64_t row, int size) {
+  return p != nullptr && aligned(p, 16) && seq_stride >= 0 && token_stride >= row && (seq_stride * size) % 16 == 0 &&
+         (token_stride * size) % 16 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+q4kv_status q4kv_append_rotary(const q4kv_pool* pool, const q4kv_rotary* rotary, const void* k, const void* v,
+                               int32_t in_dtype, int32_t batch, int32_t max_new, const int32_t* n_new,
+                               int64_t seq_stride, int64_t token_stride, const void* q, int32_t n_q_heads,
+                               int64_t q_seq_stride, int64_t q_token_stride, void* q_out, int64_t q_out_seq_stride,
+                               int64_t q_out_token_stride, const int32_t* tables, int32_t max_blocks,
+                               const int32_t* seq_lens, const int32_t* positions, void* stream) {
+  int64_t rows = 0;
+  const q4kv_status st = check_append(pool, k, v, in_dtype, batch, max_new, n_new, seq_stride, token_stride, tables,
+                                      max_blocks, seq_lens, &rows);
+  if (st != Q4KV_OK) return st;
+  if (rotary == nullptr || (rotary->interleaved != 0 && rotary->interleaved != 1) || rotary->n_axes < 1 ||
+      rotary->n_axes > Q4KV_MAX_AXES || rotary->max_positions < 1 || rotary->rot_dim < 32 || rotary->rot_dim % 32 != 0 ||
+      rotary->rot_dim > pool->head_dim || rotary->table == nullptr || !aligned(rotary->table, 16))
+    return Q4KV_ERR_INVALID_ARG;
+  for (int f = 0; f < rotary->rot_dim / 2; ++f)
+    if (rotary->axis[f] >= rotary->n_axes) return Q4KV_ERR_INVALID_ARG;
+  if (rows > 0 && pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks == 0) return Q4KV_ERR_INVALID_ARG;
+  if (positions != nullptr && !aligned(positions, 4)) return Q4KV_ERR_INVALID_ARG;
+  RotaryAppendArgs a;
+  a.q = nullptr;
+  a.q_out = nullptr;
+  a.n_q_heads = 0;
+  a.q_seq_stride = a.q_token_stride = a.o_seq_stride = a.o_token_stride = 0;
+  if (q != nullptr) {
+    if (n_q_heads < 1) return Q4KV_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(n_q_heads) * pool->head_dim;
+    if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
+        !rows_ok(q_out, q_out_seq_stride, q_out_token_stride, row, 2))
+      return Q4KV_ERR_INVALID_ARG;
+    if (q == q_out && (q_seq_stride != q_out_seq_stride || q_token_stride != q_out_token_stride))
+      return Q4KV_ERR_INVALID_ARG;
+    a.q = q;
+    a.q_out = q_out;
+    a.n_q_heads = n_q_heads;
+    a.q_seq_stride = q_seq_stride;
+    a.q_token_stride = q_token_stride;
+    a.o_seq_stride = q_out_seq_stride;
+    a.o_token_stride = q_out_token_stride;
+  }
+  if (rows == 0) return Q4KV_OK;
+  a.pool = view_of(*pool);
+  a.rot = *rotary;
+  a.k = k;
+  a.v = v;
+  a.in_dtype = in_dtype;
+  a.batch = batch;
+  a.max_new = max_new;
+  a.n_new = n_new;
+  a.seq_stride = seq_stride;
+  a.token_stride = token_stride;
+  a.tables = tables;
+  a.max_blocks = max_blocks;
+  a.seq_lens = seq_lens;
+  a.positions = positions;
+  return from_cuda(launch_append_rotary(a, as_stream(stream)));
+}
+
+q4kv_status q4kv_gather_tokens(const q4kv_pool* pool, const int32_t* tables, int32_t max_blocks, int32_t batch,
+                               const int32_t* starts, const int32_t* offsets, int64_t n_rows, void* k_out, void* v_out,
+                               int64_t out_stride, int32_t out_dtype, int32_t unrotate_k, void* stream) {
+  const q4kv_status st = check_pool(pool);
+  if (st != Q4KV_OK) return st;
+  if ((out_dtype != Q4KV_F32 && out_dtype != Q4KV_F16 && out_dtype != Q4KV_BF16) || batch < 0 || n_rows < 0 ||
+      n_rows > 0x7fffffff || (unrotate_k != 0 && unrotate_k != 1))
+    return Q4KV_ERR_INVALID_ARG;
+  const int size = out_dtype == Q4KV_F32 ? 4 : 2;
+  if (out_stride < static_cast<int64_t>(pool->n_kv_heads) * pool->head_dim || (out_stride * size) % 16 != 0)
+    return Q4KV_ERR_INVALID_ARG;
+  if (n_rows == 0 || batch == 0) return Q4KV_OK;
+  if (tables == nullptr || !aligned(tables, 4) || max_blocks < 1 || offsets == nullptr || !aligned(offsets, 4) ||
+      (starts != nullptr && !aligned(starts, 4)) || k_out == nullptr || v_out == nullptr || !aligned(k_out, 16) ||
+      !aligned(v_out, 16))
+    return Q4KV_ERR_INVALID_ARG;
+  GatherArgs a;
+  a.pool = view_of(*pool);
+  a.tables = tables;
+  a.max_blocks = max_blocks;
+  a.batch = batch;
+  a.starts = starts;
+  a.offsets = offsets;
+  a.n_rows = n_rows;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.out_stride = out_stride;
+  a.out_dtype = out_dtype;
+  a.unrotate_k = unrotate_k;
+  return from_cuda(launch_gather(a, as_stream(stream)));
+}
+
+// decode_splits < 0 lets the decode planner choose from num_sms.
+static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             int32_t max_blocks, int32_t window, int32_t n_splits, int32_t decode_splits,
+                             int32_t num_sms, q4kv_extend_plan* plan) {
+  if (plan == nullptr || batch < 0 || max_new < 0 || n_q_heads < 1 || n_kv_heads < 1 || max_blocks < 1 || window < 0 ||
+      n_splits < 0 || num_sms < 0 || n_q_heads % n_kv_heads != 0 || batch > 65535 || n_kv_heads > 65535)
+    return Q4KV_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_blocks) * kBlockTokens > 0x7fffffff ||
+      static_cast<int64_t>(batch) * max_new * n_q_heads > 0x7fffffff)
+    return Q4KV_ERR_INVALID_ARG;
+  if (head_dim != 128 && head_dim != 256) return Q4KV_ERR_UNSUPPORTED;
+  const int g = n_q_heads / n_kv_heads;
+  if (g > 64) return Q4KV_ERR_UNSUPPORTED;
+  if (num_sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return Q4KV_ERR_CUDA;
+  }
+  const int64_t group_rows = static_cast<int64_t>(max_new) * g;
+  const ExtendShape sh = extend_shape(head_dim, group_rows);
+  // the most keys a row tile can see, in steps of the streams together
+  int64_t ctx = static_cast<int64_t>(max_blocks) * kBlockTokens;
+  if (window > 0) ctx = min(ctx, static_cast<int64_t>(window) + (sh.rows + g - 1) / g + sh.tile);
+  const int64_t step = static_cast<int64_t>(sh.tile) * sh.streams;
+  const int64_t steps = (ctx + step - 1) / step;
+  int64_t s = n_splits;
+  if (s == 0) {
+    // waves of CTAs (one per SM) x (steps of an item + what starting and
+    // ending one costs, in steps)
+    const int64_t items = max(int64_t{1}, static_cast<int64_t>(batch) * n_kv_heads * ((group_rows + sh.rows - 1) / sh.rows));
+    double best = 1e300;
+    s = 1;
+    for (int64_t cand = 1; cand <= min(steps, int64_t{4} * num_sms); ++cand) {
+      const int64_t per = (steps + cand - 1) / cand;
+      if ((steps + per - 1) / per != cand) continue;
+      const double cost = static_cast<double>((items * cand + num_sms - 1) / num_sms) * (per + 4.0);
+      if (cost < best - 1e-9) {
+        best = cost;
+        s = cand;
+      }
+    }
+  }
+  s = max(int64_t{1}, min(s, steps));
+  const int64_t per = (steps + s - 1) / s;
+  s = (steps + per - 1) / per;
+  memset(plan, 0, sizeof(*plan));
+  plan->batch = batch;
+  plan->max_new = max_new;
+  plan->n_q_heads = n_q_heads;
+  plan->n_kv_heads = n_kv_heads;
+  plan->head_dim = head_dim;
+  plan->max_blocks_per_seq = max_blocks;
+  plan->window = window;
+  plan->n_splits = static_cast<int32_t>(s);
+  const int64_t partials = s * sh.streams;
+  if (partials > 1) {
+    const size_t rows = static_cast<size_t>(batch) * max_new * n_q_heads * partials;
+    plan->workspace_bytes = round_up(rows * head_dim * sizeof(float), 256) + round_up(rows * sizeof(float2), 256);
+  }
+  return Q4KV_OK;
+}
+
+q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads,
+                                  int32_t head_dim, int32_t max_blocks_per_seq, int32_t window, int32_t n_splits,
+                                  int32_t num_sms, q4kv_extend_plan* plan) {
+  return make_plan(batch, max_new, n_q_heads, n_kv_heads, head_dim, max_blocks_per_seq, window, n_splits, -1, num_sms,
+                   plan);
+}
+
+q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan* plan, const void* q, int32_t q_dtype,
+                                  int64_t q_seq_stride, int64_t q_token_stride, const int32_t* block_tables,
+                                  const int32_t* seq_lens, const int32_t* n_new, float softmax_scale, void* out,
+                                  int32_t out_dtype, int64_t out_seq_stride, int64_t out_token_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  q4kv_status st = check_pool(pool);
+  if (st != Q4KV_OK) return st;
+  if (plan == nullptr) return Q4KV_ERR_INVALID_ARG;
+  // the plan must be one q4kv_extend_plan_make would produce for this pool
+  q4kv_extend_plan ref;
+  if (plan->n_splits < 1) return Q4KV_ERR_INVALID_ARG;
+  st = make_plan(plan->batch, plan->max_new, plan->n_q_heads, plan->n_kv_heads, plan->head_dim,
+                 plan->max_blocks_per_seq, plan->window, plan->n_splits, plan->decode_splits, 1, &ref);
+  if (st != Q4KV_OK) return st;
+  if (plan->head_dim != pool->head_dim || plan->n_kv_heads != pool->n_kv_heads || ref.n_splits != plan->n_splits ||
+      ref.workspace_bytes != plan->workspace_bytes)
+    return Q4KV_ERR_INVALID_ARG;
+  if ((q_dtype != Q4KV_F16 && q_dtype != Q4KV_BF16) ||
+      (out_dtype != Q4KV_F32 && out_dtype != Q4KV_F16 && out_dtype != Q4KV_BF16) || !isfinite(softmax_scale))
+    return Q4KV_ERR_INVALID_ARG;
+  if (plan->batch == 0 || plan->max_new == 0) return Q4KV_OK;
+  const int64_t row = static_cast<int64_t>(plan->n_q_heads) * plan->head_dim;
+  if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
+      !rows_ok(out, out_seq_stride, out_token_stride, row, out_dtype == Q4KV_F32 ? 4 : 2))
+    return Q4KV_ERR_INVALID_ARG;
+  if (block_tables == nullptr || !aligned(block_tables, 16) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
+      (n_new != nullptr && !aligned(n_new, 4)))
+    return Q4KV_ERR_INVALID_ARG;
+  if (pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks == 0) return Q4KV_ERR_INVALID_ARG;
+  if (plan->workspace_bytes > 0 &&
+      (workspace == nullptr || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256)))
+    return Q4KV_ERR_WORKSPACE;
+  ExtendArgs a;
+  a.pool = view_of(*pool);
+  a.plan = *plan;
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.q_seq_stride = q_seq_stride;
+  a.q_token_stride = q_token_stride;
+  a.tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.n_new = n_new;
+  a.scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(plan->head_dim));
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.o_seq_stride = out_seq_stride;
+  a.o_token_stride = out_token_stride;
+  a.ws_o = nullptr;
+  a.ws_ml = nullptr;
+  return from_cuda(launch_extend(a, as_stream(stream)));
+}
+
+}  // extern "C"
