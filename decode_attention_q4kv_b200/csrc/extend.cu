@@ -1,137 +1,704 @@
 // Attention of a chunk of new tokens over the paged quantised cache.
 //
-// One warp per query row: a lane holds D/32 consecutive channels; keys and
-// values are decoded as they are read, the softmax keeps a running maximum and
-// sum in binary32.
+// For the rows (token i, head of the group) of one KV head:
+//   o = sum_t p_t V_t / sum_t p_t,  p_t = 2^(s_t - m),  s_t = log2(e) scale <q, K_t>
+// over the positions t the token sees.  A CTA holds 128 or 256 rows; it walks
+// their keys in tiles, S = Q K^T and O += P V on the tensor cores (fp16
+// operands, fp32 accumulators in tensor memory).
+//
+// Warp roles (18 warps):
+//   feed     one thread copies each tile's packed codes, scales and mask into a
+//            ring in shared memory (bulk copies)
+//   decode   eight warps turn a tile's codes into fp16 and write it in the
+//            layout the tensor cores read (rows of 128 bytes, 128-byte swizzle);
+//            remapped slots and slots past the end become zeros
+//   product  one thread issues the matrix products
+//   softmax  eight warps, one row per thread: maximum, weights, sum.  The
+//            weights go back into the tensor memory that held the logits, and
+//            are the A operand of the second product.
+// Within 8 channels the decoded order is 0 4 1 5 2 6 3 7 (what one mask and one
+// subtraction per pair of codes leave); q is stored in the same order and the
+// output's columns are put back when they are written.
+//
+// Roundings: K and V to fp16 (one fused multiply-add code * s + z), q to fp16
+// after a power-of-two scaling per row, the weights to fp16 (scaled by 2^6, so
+// that weights down to 2^-30 of the largest survive); each is at most 2^-11
+// relative.  Maxima, sums and accumulators are binary32.  The running maximum
+// is only moved when it grows by more than 2^8: until then weights above 1 are
+// harmless (at most 2^14 in fp16), and the accumulator is not rescaled.
 #include <math.h>
 
+#include "encode.cuh"
 #include "extend_internal.cuh"
+#include "tcgen05.cuh"
 
 namespace q4kv {
 namespace {
 
-template <int D>
-__device__ __forceinline__ void load_row(const PoolView& P, bool key, int blk, int h, int slot, int lane,
-                                         float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  const int bits = P.bits_of(blk);
-  const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
-  const int64_t row = (phys * P.n_kv_heads + h) * kBlockTokens + slot;
-  const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
-                                   : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
-  const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
-                                    : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
-  codes += row * (D * bits / 8);
-  float s = 1.0f, z = 0.0f;
-  if (!P.fp8) {
-    const __half2 p = params[row * (D / kGroup) + lane * E / kGroup];
-    s = __low2float(p);
-    z = __high2float(p);
-  }
+constexpr int kDecodeWarp0 = 8, kMmaWarp = 16, kFeedWarp = 17;
+constexpr int kThreads = 18 * 32;
+constexpr int kDecodeWarps = 8;
+constexpr float kShift = 6.0f;   // weights are stored times 2^6
+constexpr float kLazy = 8.0f;    // growth of the maximum (log2) that moves it
+constexpr float kLog2e = 1.4426950408889634f;
+
+// MODE 0: D = 128, two row tiles of 128, each with its softmax warps.
+// MODE 1: D = 128, one row tile; the two sets of softmax warps take alternate
+//         key tiles with their own accumulators (two partial results).
+// MODE 2: D = 256, one row tile, key tiles of 64 with two logit buffers.
+template <int MODE>
+struct Geo {
+  static constexpr int D = MODE == 2 ? 256 : 128;
+  static constexpr int BN = MODE == 2 ? 64 : 128;      // tokens of a key tile
+  static constexpr int QT = MODE == 0 ? 2 : 1;         // row tiles
+  static constexpr int STREAMS = MODE == 1 ? 2 : 1;    // partial results of a row
+  static constexpr int R = 128 * QT;
+  static constexpr int SLOTS = MODE == 1 ? 4 : 3;      // decoded tiles
+  static constexpr uint32_t kTile = BN * D * 2;        // bytes of a decoded tile
+  static constexpr uint32_t kQ = QT * 128 * D * 2;
+  static constexpr uint32_t kSBase = 256;              // tensor-memory columns: O from 0, S from here
+};
+constexpr uint32_t kRawRing = 65536;
+constexpr uint32_t kRawAt = 163840;                    // Q and the decoded tiles fill this in every mode
+constexpr uint32_t kMiscAt = kRawAt + kRawRing;
+constexpr uint32_t kSmem = kMiscAt + 2048;
+static_assert(Geo<0>::kQ + Geo<0>::SLOTS * Geo<0>::kTile == kRawAt && Geo<1>::kQ + Geo<1>::SLOTS * Geo<1>::kTile == kRawAt &&
+              Geo<2>::kQ + Geo<2>::SLOTS * Geo<2>::kTile == kRawAt, "shared memory layout");
+constexpr int kMaxRaw = 7;
+
+struct Misc {
+  uint64_t raw_full[8], raw_empty[8], kv_full[4], kv_empty[4], s_full[2], p_full[2], o_done[2], spare;
+  uint32_t tmem;
+  int abort;
+  int raw_bits[8];      // code width of the tile in a ring entry, 0 = a block id out of range
+  float rs[256];        // per row: log2(e) * scale * 2^exponent
+};
+static_assert(sizeof(Misc) <= 2048, "misc area");
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+
+// Bounded wait; on running out the CTA gives up (abort), every other wait
+// runs out in turn.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* ms) {
+  if (mbar_wait(bar, parity)) return true;
+  *reinterpret_cast<volatile int*>(&ms->abort) = 1;
+  return false;
+}
+
+// The same by a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Misc* ms) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, ms));
+}
+
+// 32 codes of one token, channels c .. c+31 of one group, as 16 half pairs in
+// the order above: fp16(code * s + z).
+__device__ __forceinline__ void decode32(int bits, bool fp8, const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
+  const __half2 k1024 = __float2half2_rn(1024.0f);
+  if (fp8) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int c = lane * E + e;
-    if (P.fp8) {
-      __nv_fp8_e4m3 f;
-      f.__x = codes[c];
-      x[e] = static_cast<float>(f);
-    } else {
-      const int v = bits == 8 ? codes[c] : bits == 4 ? (codes[c / 2] >> (4 * (c & 1))) & 15 : (codes[c / 4] >> (2 * (c & 3))) & 3;
-      x[e] = __fmaf_rn(static_cast<float>(v), s, z);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | (4 + i) << 4));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
+        o[4 * c + i] = h2u(*reinterpret_cast<const __half2*>(&h));
+      }
+  } else if (bits == 4) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    const __half2 k16 = __float2half2_rn(0.0625f), k64 = __float2half2_rn(-64.0f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v = w[c] >> (8 * i);
+        const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);         // 1024 + code, exact
+        const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);      // (1024 + 16 code) / 16 - 64
+        o[4 * c + 2 * i] = h2u(__hfma2(lo, s, z));
+        o[4 * c + 2 * i + 1] = h2u(__hfma2(hi, s, z));
+      }
+  } else if (bits == 8) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
+        o[4 * c + i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), k1024), s, z));
+      }
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = c < 2 ? a.x : a.y;
+      const uint32_t v = __byte_perm(x, 0, c & 1 ? 0x4342 : 0x4140);                     // codes 0-3, codes 4-7
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = 1.0f / static_cast<float>(1 << (2 * i));
+        const __half2 h = __hfma2(u2h((v & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
+                                  __float2half2_rn(-1024.0f * f));
+        o[4 * c + i] = h2u(__hfma2(h, s, z));
+      }
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) extend_simple_kernel(const __grid_constant__ ExtendArgs a, int64_t n_rows) {
-  constexpr int E = D / 32;
+// Output columns 8k .. 8k+7 back in channel order.
+__device__ __forceinline__ void channel_order(const uint32_t (&r)[32], float f, float (&y)[32]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[8 * k + i] = __uint_as_float(r[8 * k + 2 * i]) * f;
+      y[8 * k + 4 + i] = __uint_as_float(r[8 * k + 2 * i + 1]) * f;
+    }
+}
+__device__ __forceinline__ void store32(void* out, int dtype, int64_t at, const float (&y)[32]) {
+  if (dtype == Q4KV_F32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+    return;
+  }
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (dtype == Q4KV_F16) {
+      w[i] = h2u(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  uint4* o = reinterpret_cast<uint4*>(static_cast<__half*>(out) + at);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// The part of the work one CTA has; every thread computes the same.
+struct Item {
+  int b, h, split;
+  int g, T;
+  int len, nn;         // cached tokens, new tokens
+  int r0, r1, rv;      // rows of the tile, end of the rows there are, end of the rows of real tokens
+  int t0, n;           // first token of the first key tile, key tiles
+  bool bad;
+};
+template <int MODE>
+__device__ __forceinline__ Item item_of(const ExtendArgs& a) {
+  using G = Geo<MODE>;
+  Item w;
+  const int S = a.plan.n_splits;
+  w.T = a.plan.max_new;
+  w.g = a.plan.n_q_heads / a.pool.n_kv_heads;
+  w.h = blockIdx.y;
+  w.b = blockIdx.z;
+  // later row tiles see more keys and start first
+  const int tile = static_cast<int>((gridDim.x - 1 - blockIdx.x) / S);
+  w.split = static_cast<int>((gridDim.x - 1 - blockIdx.x) % S);
+  w.len = __ldg(a.seq_lens + w.b);
+  w.nn = a.n_new == nullptr ? w.T : max(0, min(__ldg(a.n_new + w.b), w.T));
+  w.bad = w.len < 0 || static_cast<int64_t>(w.len) + w.nn > static_cast<int64_t>(a.plan.max_blocks_per_seq) * kBlockTokens;
+  w.r0 = tile * G::R;
+  w.r1 = min(w.r0 + G::R, w.T * w.g);
+  w.rv = min(w.r1, w.nn * w.g);
+  w.t0 = w.n = 0;
+  if (w.bad || w.rv <= w.r0) return w;
+  const int end = w.len + (w.rv - 1) / w.g + 1;
+  const int begin = a.plan.window > 0 ? max(0, w.len + w.r0 / w.g - a.plan.window + 1) : 0;
+  const int first = begin / G::BN, tiles = (end + G::BN - 1) / G::BN - first;
+  const int steps = (tiles + G::STREAMS - 1) / G::STREAMS, per = (steps + S - 1) / S;
+  const int j0 = min(tiles, w.split * per * G::STREAMS), j1 = min(tiles, (w.split + 1) * per * G::STREAMS);
+  w.t0 = (first + j0) * G::BN;
+  w.n = j1 - j0;
+  return w;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ ExtendArgs a, uint32_t raw_stride,
+                                                             int n_raw) {
+  using G = Geo<MODE>;
+  constexpr int D = G::D, BN = G::BN;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  griddep_wait();
+  griddep_launch_dependents();
   const PoolView& P = a.pool;
-  const int lane = threadIdx.x & 31;
-  const int hq = a.plan.n_q_heads, g = hq / P.n_kv_heads, T = a.plan.max_new, mb = a.plan.max_blocks_per_seq;
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (row >= n_rows) return;
-  const int h = static_cast<int>(row % hq), i = static_cast<int>(row / hq % T), b = static_cast<int>(row / hq / T);
-  const int len = a.seq_lens[b], nn = a.n_new == nullptr ? T : min(a.n_new[b], T);
-  bool ok = i < nn;
-  if (ok && (len < 0 || static_cast<int64_t>(len) + nn > static_cast<int64_t>(mb) * kBlockTokens)) {
-    if (lane == 0) raise_error(P.error_word, Q4KV_DEVERR_SEQ_LEN);
-    ok = false;
-  }
-  float acc[E] = {}, m = -INFINITY, l = 0.0f;
-  if (ok) {
-    float q[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int64_t at = b * a.q_seq_stride + i * a.q_token_stride + static_cast<int64_t>(h) * D + lane * E + e;
-      q[e] = a.q_dtype == Q4KV_F16 ? __half2float(static_cast<const __half*>(a.q)[at])
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
+  Misc* ms = reinterpret_cast<Misc*>(sm + kMiscAt);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Item w = item_of<MODE>(a);
+  const int hq = a.plan.n_q_heads, S = a.plan.n_splits, mb = a.plan.max_blocks_per_seq;
+  const int partials = S * G::STREAMS;
+  const int64_t all_rows = static_cast<int64_t>(a.plan.batch) * w.T * hq;
+
+  if (w.bad && w.nn > 0 && tid == 0) raise_error(P.error_word, Q4KV_DEVERR_SEQ_LEN);
+  if (partials == 1) {   // rows of no real token are 0 (the merge sees to them otherwise)
+    const int z0 = w.bad ? w.r0 : max(w.r0, w.rv);
+    for (int x = tid; x < (w.r1 - z0) * (D / 32); x += kThreads) {
+      const int r = z0 + x / (D / 32);
+      const float zero[32] = {};
+      store32(a.out, a.out_dtype, w.b * a.o_seq_stride + (r / w.g) * a.o_token_stride +
+              static_cast<int64_t>(w.h * w.g + r % w.g) * D + (x % (D / 32)) * 32, zero);
     }
-    if (P.k_rotated) {
+  }
+  if (w.bad || w.rv <= w.r0) return;
+  if (w.n == 0) {        // no keys in this split
+    for (int x = tid; x < (w.rv - w.r0) * G::STREAMS; x += kThreads) {
+      const int r = w.r0 + x / G::STREAMS;
+      const int64_t row = (static_cast<int64_t>(w.b) * w.T + r / w.g) * hq + w.h * w.g + r % w.g;
+      a.ws_ml[(w.split * G::STREAMS + x % G::STREAMS) * all_rows + row] = make_float2(-INFINITY, 0.0f);
+    }
+    return;
+  }
+
+  // softmax warps with real rows, per row tile; MODE 0 drops its second tile
+  // when no row is in it
+  const int warps0 = min(4, (w.rv - w.r0 + 31) / 32);
+  const int warps1 = MODE == 0 ? max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32)) : warps0;
+  const int lag = MODE == 0 && warps1 == 0 ? 1 : 2;       // logit buffers in use
+  const int units = w.n * (MODE == 0 ? lag : 1);          // (row tile, key tile) products
+
+  if (tid == 0) {
+    for (int i = 0; i < n_raw; ++i) {
+      mbar_init(&ms->raw_full[i], 1);
+      mbar_init(&ms->raw_empty[i], kDecodeWarps);
+    }
+    for (int i = 0; i < G::SLOTS; ++i) {
+      mbar_init(&ms->kv_full[i], kDecodeWarps);
+      mbar_init(&ms->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms->s_full[i], 1);
+      mbar_init(&ms->p_full[i], MODE != 0 ? warps0 : (i == 0 ? warps0 : max(1, warps1)));
+      mbar_init(&ms->o_done[i], 1);
+    }
+    mbar_init(&ms->spare, 1);
+    ms->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) tmem_alloc(&ms->tmem, 512);
+
+  // Q: rotate, scale each row by a power of two, round to fp16
+  {
+    using Sh = Shape<D>;
+    const int r = lane / Sh::LPV, j = lane % Sh::LPV;
+    for (int p = warp; p < G::R / Sh::VPW; p += kThreads / 32) {
+      const int row = p * Sh::VPW + r, rr = w.r0 + row;
+      float2 x[8];
 #pragma unroll
-      for (int st = 1; st < E; st <<= 1)
+      for (int i = 0; i < 8; ++i) x[i] = make_float2(0.0f, 0.0f);
+      if (rr < w.rv) {
+        const int64_t at = w.b * a.q_seq_stride + (rr / w.g) * a.q_token_stride +
+                           static_cast<int64_t>(w.h * w.g + rr % w.g) * D + j * kEPL;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at);
+        const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
+        if (a.q_dtype == Q4KV_F16) unpack16<__half>(w0, w1, x);
+        else unpack16<__nv_bfloat16>(w0, w1, x);
+      }
+      __syncwarp();
+      if (P.k_rotated) {
+        rotate_pairs<D>(x, j);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if ((e & st) == 0) {
-            const float x = q[e], y = q[e + st];
-            q[e] = x + y;
-            q[e + st] = x - y;
-          }
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x * kRotScale<D>, x[i].y * kRotScale<D>);
+      }
+      float m = 0.0f;
 #pragma unroll
-      for (int st = 1; st < 32; st <<= 1)
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float o = __shfl_xor_sync(0xffffffffu, q[e], st);
-          q[e] = lane & st ? o - q[e] : q[e] + o;
+      for (int st = 1; st < Sh::LPV; st <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, st));
+      // the row's largest magnitude comes to lie in [64, 128)
+      const int e = m == 0.0f ? 0 : max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
+      const float f = __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
+      if (j == 0) ms->rs[row] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e - 6) << 23);
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] = h2u(__floats2half2_rn(x[i].x * f, x[i + 4].x * f));
+        o[4 + i] = h2u(__floats2half2_rn(x[i].y * f, x[i + 4].y * f));
+      }
+      const int lr = row & 127;
+      uint8_t* base = sm + (row >> 7) * (128 * D * 2) + (j >> 2) * (128 * 128) + (lr >> 3) * 1024 + (lr & 7) * 128;
+      const int c = (2 * j) & 7;
+      *reinterpret_cast<uint4*>(base + ((c ^ (lr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(base + (((c + 1) ^ (lr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+  fence_async_shared();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  const int end = w.len + w.nn;                            // tokens of the sequence
+  const int32_t* table = a.tables + static_cast<int64_t>(w.b) * mb;
+
+  if (warp == kFeedWarp) {
+    // ---- feed ------------------------------------------------------------------
+    if (lane == 0) {
+      int issued = 0;
+      bool ok = true;
+      for (int n = 0; n < 2 * w.n && ok; ++n) {
+        const int t = w.t0 + (n >> 1) * BN, e = n % n_raw;
+        const int blk = __ldg(table + t / kBlockTokens);
+        ok = wait_or_abort(&ms->raw_empty[e], ((n / n_raw) & 1) ^ 1, ms);
+        if (!ok) break;
+        uint8_t* dst = sm + kRawAt + e * raw_stride;
+        if (blk < 0 || blk >= P.n_blocks()) {
+          raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
+          ms->raw_bits[e] = 0;
+          mbar_arrive(&ms->raw_full[e]);
+        } else {
+          const int bits = P.bits_of(blk);
+          const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
+          const int64_t row = (phys * P.n_kv_heads + w.h) * kBlockTokens + t % kBlockTokens;
+          const bool key = (n & 1) == 0;
+          const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
+                                           : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
+          const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
+                                            : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
+          const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
+          ms->raw_bits[e] = bits;
+          mbar_arrive_tx(&ms->raw_full[e], cb + pb + 16);
+          bulk_g2s(dst, codes + row * (D / 8 * bits), cb, &ms->raw_full[e]);
+          if (!P.fp8) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, &ms->raw_full[e]);
+          bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16,
+                   &ms->raw_full[e]);
         }
-#pragma unroll
-      for (int e = 0; e < E; ++e) q[e] *= rotation_constant(D);
+        issued = n + 1;
+      }
+      if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)        // let the copies in flight land
+        for (int n = max(0, issued - n_raw); n < issued; ++n) mbar_wait(&ms->raw_full[n % n_raw], (n / n_raw) & 1);
     }
-    const int end = len + i;
-    for (int t = a.plan.window > 0 ? max(0, end - a.plan.window + 1) : 0; t <= end; ++t) {
-      const int blk = a.tables[static_cast<int64_t>(b) * mb + t / kBlockTokens];
-      if (blk < 0 || blk >= P.n_blocks()) {
-        if (lane == 0) raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
-        ok = false;
-        break;
+  } else if (warp == kMmaWarp) {
+    // ---- product ---------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kQk = mma_f16_desc(128, BN, false), kPv = mma_f16_desc(128, D, true);
+      const uint32_t q_at = smem_u32(sm), kv_at = q_at + G::kQ;
+      bool ok = true;
+      for (int u = 0; u < units + lag && ok; ++u) {
+        if (u >= lag) {                                    // O += P V of unit v
+          const int v = u - lag, buf = v % lag;
+          const int j = MODE == 0 ? v / lag : v, n = 2 * j + 1, slot = n % G::SLOTS;
+          ok = wait_or_abort(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms) && wait_or_abort(&ms->p_full[buf], (v / lag) & 1, ms);
+          if (!ok) break;
+          tc_fence_after();
+          const int oi = MODE == 2 ? 0 : buf;
+          const uint32_t at = kv_at + slot * G::kTile;
+          const bool first = MODE == 2 ? v == 0 : v < lag;
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            mma_ts(tmem + oi * 128, tmem + G::kSBase + buf * BN + k * 8, smem_operand(at + k * 2048, BN * 128, 1024), kPv,
+                   !first || k > 0);
+          mma_commit(&ms->o_done[oi]);
+          if (MODE != 0 || v % lag == lag - 1) mma_commit(&ms->kv_empty[slot]);
+        }
+        if (u < units) {                                   // S = Q K^T of unit u
+          const int buf = u % lag;
+          const int j = MODE == 0 ? u / lag : u, n = 2 * j, slot = n % G::SLOTS;
+          ok = wait_or_abort(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t q = q_at + (MODE == 0 ? buf * (128 * D * 2) : 0), at = kv_at + slot * G::kTile;
+          // (the product that read the weights in this buffer was issued
+          // before this one; products of one thread run in order)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + G::kSBase + buf * BN, smem_operand(q + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                   smem_operand(at + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), kQk, k > 0);
+          mma_commit(&ms->s_full[buf]);
+          if (MODE != 0 || u % lag == lag - 1) mma_commit(&ms->kv_empty[slot]);
+        }
       }
-      const int slot = t % kBlockTokens;
-      const bool gone = (P.mask[static_cast<int64_t>(blk) * kMaskWords + slot / 32] >> (slot % 32)) & 1u;
-      float s = Q4KV_SENTINEL_LOGIT, x[E] = {};
-      if (!gone) {
-        load_row<D>(P, true, blk, h / g, slot, lane, x);
-        s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += q[e] * x[e];
-#pragma unroll
-        for (int st = 1; st < 32; st <<= 1) s += __shfl_xor_sync(0xffffffffu, s, st);
-        s *= a.scale;
-        load_row<D>(P, false, blk, h / g, slot, lane, x);
+      if (!ok) {
+        mma_commit(&ms->spare);
+        mbar_wait(&ms->spare, 0);
       }
-      const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-      l = l * c + p;
+    }
+    __syncwarp();
+  } else if (warp >= kDecodeWarp0) {
+    // ---- decode ----------------------------------------------------------------
+    const int dw = warp - kDecodeWarp0;
+    // a warp takes 8 tokens x 128 channels or 4 x 256 at a time, a lane 32
+    // channels of one token; the tokens are skewed over the lanes so that both
+    // the reads of codes and the swizzled writes are free of bank conflicts
+    const int u = D == 128 ? lane & 3 : lane & 7;
+    const int tl = D == 128 ? (((lane >> 2) & 1) + 2 * (u >> 1) + 2 * (lane >> 3)) & 7 : ((u >> 1) + (lane >> 3)) & 3;
+    bool ok = true;
+    for (int n = 0; n < 2 * w.n && ok; ++n) {
+      const int e = n % n_raw, slot = n % G::SLOTS;
+      ok = warp_wait(&ms->raw_full[e], (n / n_raw) & 1, ms) && warp_wait(&ms->kv_empty[slot], ((n / G::SLOTS) & 1) ^ 1, ms);
+      if (!ok) break;
+      const int bits = ms->raw_bits[e];
+      const uint8_t* raw = sm + kRawAt + e * raw_stride;
+      const __half2* params = reinterpret_cast<const __half2*>(raw + raw_stride - 16 - BN * (D / kGroup) * 4);
+      const uint32_t* mask = reinterpret_cast<const uint32_t*>(raw + raw_stride - 16);
+      const int t0 = w.t0 + (n >> 1) * BN;
+      uint8_t* dst = sm + G::kQ + slot * G::kTile + (u >> 1) * (BN * 128);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * c + (gone ? 0.0f : p * x[e]);
-      m = mn;
+      for (int it = 0; it < 2; ++it) {
+        const int t = (it * kDecodeWarps + dw) * (D == 128 ? 8 : 4) + tl;
+        uint32_t o[16];
+        const int mt = (t0 + t) & 127;
+        const bool live = bits != 0 && t0 + t < end && !((mask[mt >> 5] >> (mt & 31)) & 1u);
+        if (live) {
+          const __half2 sz = P.fp8 ? __half2() : params[t * (D / kGroup) + (u >> 1)];
+          decode32(bits, P.fp8, raw + (t * D + u * 32) / 8 * bits, __low2half2(sz), __high2half2(sz), o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0;
+        }
+        uint8_t* row = dst + (t >> 3) * 1024 + (t & 7) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(row + (((4 * (u & 1) + i) ^ (t & 7)) << 4)) =
+              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ms->raw_empty[e]);
+        mbar_arrive(&ms->kv_full[slot]);
+      }
+    }
+  } else if ((MODE == 2 ? warp < 4 : true) && (warp & 3) < (warp < 4 ? warps0 : warps1)) {
+    // ---- softmax ---------------------------------------------------------------
+    const int st = MODE == 2 ? 0 : warp >> 2;              // stream
+    const int local = (MODE == 0 ? st * 128 : 0) + (warp & 3) * 32 + lane;
+    const int r = w.r0 + local;
+    const bool real = r < w.rv;
+    const int pos = w.len + min(r, w.rv - 1) / w.g;        // the row's position
+    const float rs = ms->rs[local];
+    const float sent = Q4KV_SENTINEL_LOGIT * kLog2e / rs;  // a remapped slot's logit before scaling
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_at = tmem + lanes + (MODE == 2 ? 0 : st * 128);
+    const int steps = MODE == 1 ? (w.n - st + 1) / 2 : w.n;
+    float m = -INFINITY, l = 0.0f;
+    bool poison = false, ok = true;
+
+    for (int k = 0; k < steps; ++k) {
+      const int buf = MODE == 2 ? k & 1 : st;
+      const uint32_t phase = (MODE == 2 ? k >> 1 : k) & 1;
+      const int t0 = w.t0 + (MODE == 1 ? 2 * k + st : k) * BN;
+      const uint32_t s_at = tmem + lanes + G::kSBase + buf * BN;
+      uint32_t gone[BN / 32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) gone[c] = 0;
+      const int blk = __ldg(table + t0 / kBlockTokens);
+      const bool bad = blk < 0 || blk >= P.n_blocks();
+      uint32_t any = 0;
+      if (!bad) {
+        const uint32_t* mw = P.mask + static_cast<int64_t>(blk) * kMaskWords + (t0 % kBlockTokens) / 32;
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) any |= gone[c] = __ldg(mw + c);
+      }
+      const int hi = pos - t0;                             // last column the row sees
+      const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
+      if (bad && hi >= 0 && lo < BN) poison = true;
+      const bool plain = __all_sync(0xffffffffu, hi >= BN - 1 && lo <= 0 && any == 0);
+      ok = warp_wait(&ms->s_full[buf], phase, ms);
+      if (!ok) break;
+      tc_fence_after();
+
+      uint32_t x[32];
+      // logits of columns 32c .. 32c+31, with the mask applied
+      auto load = [&](int c) {
+        tmem_ld32(s_at + 32 * c, x);
+        tmem_wait_ld();
+        if (!plain) {
+          const int h1 = hi - 32 * c, l1 = lo - 32 * c;
+          uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
+          seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float y = (gone[c] >> i) & 1u ? sent : __uint_as_float(x[i]);
+            x[i] = __float_as_uint((seen >> i) & 1u ? y : -INFINITY);
+          }
+        }
+      };
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        load(c);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      }
+      const float top = fmaxf(m, mx * rs);
+      if (k == 0) {
+        m = top;
+      } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
+        // move the maximum: rescale the accumulator and the sum
+        ok = warp_wait(&ms->o_done[MODE == 2 ? 0 : st], (k - 1) & 1, ms);
+        if (!ok) break;
+        tc_fence_after();
+        const float f = top == -INFINITY ? 1.0f : exp2_fast(m - top);
+        l *= f;
+        m = top;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          tmem_ld32(o_at + 32 * c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+          tmem_st32(o_at + 32 * c, x);
+        }
+        tmem_wait_st();
+      }
+      const float off = kShift - (m == -INFINITY ? 0.0f : m);
+      float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        load(c);
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float p0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), rs, off));
+          const float p1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), rs, off));
+          sum0 += p0;
+          sum1 += p1;
+          p[i] = h2u(__floats2half2_rn(p0, p1));
+        }
+        tmem_st16(s_at + 16 * c, p);
+      }
+      l += sum0 + sum1;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->p_full[buf]);
+    }
+
+    // ---- result ----------------------------------------------------------------
+    if (ok && steps > 0) ok = warp_wait(&ms->o_done[MODE == 2 ? 0 : st], (steps - 1) & 1, ms);
+    tc_fence_after();
+    const int i = r / w.g, head = w.h * w.g + r % w.g;
+    const int64_t row = (static_cast<int64_t>(w.b) * w.T + i) * hq + head;
+    const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? st : 0)) * all_rows + row;
+    const bool fine = ok && !poison && l > 0.0f;
+    if (partials > 1 && real) a.ws_ml[part] = make_float2(ok ? m : 0.0f, ok && !poison ? l : -1.0f);
+    if (ok && steps > 0) {
+      const float f = partials > 1 ? 1.0f : (fine ? 1.0f / l : 0.0f);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        float y[32];
+        tmem_ld32(o_at + 32 * c, x);
+        tmem_wait_ld();
+        channel_order(x, f, y);
+        if (partials == 1 && !fine) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+        }
+        if (real) {
+          if (partials > 1) store32(a.ws_o, Q4KV_F32, part * D + 32 * c, y);
+          else store32(a.out, a.out_dtype, w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + 32 * c, y);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (tid == 0 && ms->abort != 0) raise_error(P.error_word, Q4KV_DEVERR_TIMEOUT);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// Merge of a row's partial results; a warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExtendArgs a, int partials, int64_t rows) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int hq = a.plan.n_q_heads, T = a.plan.max_new;
+  const int head = static_cast<int>(row % hq), i = static_cast<int>(row / hq % T), b = static_cast<int>(row / hq / T);
+  const int len = __ldg(a.seq_lens + b), nn = a.n_new == nullptr ? T : max(0, min(__ldg(a.n_new + b), T));
+  const bool real = i < nn && len >= 0 && static_cast<int64_t>(len) + nn <= static_cast<int64_t>(a.plan.max_blocks_per_seq) * kBlockTokens;
+  constexpr int E = D / 32;
+  float acc[E] = {}, L = 0.0f, M = -INFINITY;
+  bool poison = false;
+  if (real) {
+    for (int p = lane; p < partials; p += 32) {
+      const float2 v = a.ws_ml[p * rows + row];
+      M = fmaxf(M, v.x);
+      poison |= v.y < 0.0f;
+    }
+#pragma unroll
+    for (int st = 1; st < 32; st <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, st));
+    poison = __any_sync(0xffffffffu, poison);
+    if (!poison && M != -INFINITY) {
+      for (int p = 0; p < partials; ++p) {
+        const float2 v = a.ws_ml[p * rows + row];
+        if (v.x == -INFINITY) continue;                     // saw no keys; its accumulator may not be written
+        const float f = exp2f(v.x - M);
+        L = fmaf(v.y, f, L);
+        const float* o = a.ws_o + (p * rows + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o + e);
+          acc[e] = fmaf(x.x, f, acc[e]);
+          acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+          acc[e + 2] = fmaf(x.z, f, acc[e + 2]);
+          acc[e + 3] = fmaf(x.w, f, acc[e + 3]);
+        }
+      }
     }
   }
+  const float f = L > 0.0f ? 1.0f / L : 0.0f;
+  const int64_t at = b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int64_t at = b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(h) * D + lane * E + e;
-    const float y = ok ? acc[e] / l : 0.0f;
-    if (a.out_dtype == Q4KV_F32) static_cast<float*>(a.out)[at] = y;
-    else if (a.out_dtype == Q4KV_F16) static_cast<__half*>(a.out)[at] = __float2half_rn(y);
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+  for (int e = 0; e < E; e += 4) {
+    const float y[4] = {acc[e] * f, acc[e + 1] * f, acc[e + 2] * f, acc[e + 3] * f};
+    if (a.out_dtype == Q4KV_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + e) = make_float4(y[0], y[1], y[2], y[3]);
+    } else if (a.out_dtype == Q4KV_F16) {
+      *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at + e) =
+          make_uint2(h2u(__floats2half2_rn(y[0], y[1])), h2u(__floats2half2_rn(y[2], y[3])));
+    } else {
+      const __nv_bfloat162 u = __floats2bfloat162_rn(y[0], y[1]), v = __floats2bfloat162_rn(y[2], y[3]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at + e) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+    }
   }
+}
+
+template <int MODE>
+cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
+  using G = Geo<MODE>;
+  const q4kv_extend_plan& p = a.plan;
+  const int64_t group_rows = static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads);
+  const int64_t x = (group_rows + G::R - 1) / G::R * p.n_splits;
+  if (x > 0x7fffffff) return cudaErrorInvalidValue;
+  const uint32_t codes = G::BN * G::D / 8 * (a.pool.n_q8 > 0 ? 8 : 4);
+  const uint32_t stride = codes + G::BN * (G::D / kGroup) * 4 + 16;
+  const int n_raw = min(kMaxRaw, static_cast<int>(kRawRing / stride));
+  cudaError_t e = cudaFuncSetAttribute(extend_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(extend_kernel<MODE>, dim3(static_cast<unsigned>(x), p.n_kv_heads, p.batch), dim3(kThreads), kSmem, stream, a,
+                 stride, n_raw);
+  if (e != cudaSuccess) return e;
+  const int partials = p.n_splits * G::STREAMS;
+  if (partials == 1) return cudaSuccess;
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.max_new * p.n_q_heads;
+  return launch_pdl(extend_merge_kernel<G::D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, a, partials,
+                    rows);
 }
 
 }  // namespace
 
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.plan.batch) * a.plan.max_new * a.plan.n_q_heads;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (a.plan.head_dim == 128) extend_simple_kernel<128><<<grid, 256, 0, stream>>>(a, rows);
-  else extend_simple_kernel<256><<<grid, 256, 0, stream>>>(a, rows);
-  return cudaGetLastError();
+  const q4kv_extend_plan& p = a.plan;
+  const ExtendShape sh = extend_shape(p.head_dim, static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads));
+  if (p.head_dim == 256) return launch_mode<2>(a, stream);
+  return sh.rows == 256 ? launch_mode<0>(a, stream) : launch_mode<1>(a, stream);
 }
 
 }  // namespace q4kv

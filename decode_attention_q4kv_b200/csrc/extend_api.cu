@@ -230,8 +230,14 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   a.out_dtype = out_dtype;
   a.o_seq_stride = out_seq_stride;
   a.o_token_stride = out_token_stride;
-  a.ws_o = nullptr;
-  a.ws_ml = nullptr;
+  a.ws_o = static_cast<float*>(workspace);
+  const size_t partial_rows = static_cast<size_t>(plan->batch) * plan->max_new * plan->n_q_heads * plan->n_splits *
+                              extend_shape(plan->head_dim, static_cast<int64_t>(plan->max_new) *
+                                                               (plan->n_q_heads / plan->n_kv_heads)).streams;
+  a.ws_ml = plan->workspace_bytes > 0
+                ? reinterpret_cast<float2*>(static_cast<char*>(workspace) +
+                                            round_up(partial_rows * plan->head_dim * sizeof(float), 256))
+                : nullptr;
   return from_cuda(launch_extend(a, as_stream(stream)));
 }
 
