@@ -9,7 +9,7 @@
 // Warp roles (18 warps):
 //   feed     one thread copies each tile's packed codes, scales and mask into a
 //            ring in shared memory (bulk copies)
-//   decode   eight warps turn a tile's codes into fp16 and write it in the
+//   decode   four warps turn the keys' codes into fp16, four the values', in the
 //            layout the tensor cores read (rows of 128 bytes, 128-byte swizzle);
 //            remapped slots and slots past the end become zeros
 //   product  one thread issues the matrix products
@@ -41,6 +41,7 @@ constexpr int kDecodeWarps = 8;
 constexpr float kShift = 6.0f;   // weights are stored times 2^6
 constexpr float kLazy = 8.0f;    // growth of the maximum (log2) that moves it
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 
 // MODE 0: D = 128, two row tiles of 128, each with its softmax warps.
 // MODE 1: D = 128, one row tile; the two sets of softmax warps take alternate
@@ -67,7 +68,13 @@ static_assert(Geo<0>::kQ + Geo<0>::SLOTS * Geo<0>::kTile == kRawAt && Geo<1>::kQ
 constexpr int kMaxRaw = 7;
 
 struct Misc {
-  uint64_t raw_full[8], raw_empty[8], kv_full[4], kv_empty[4], s_full[2], p_full[2], o_done[2], spare;
+  // Copy n (keys and values in turn) completes raw_full[n % (2 * entries)] and
+  // frees kv_empty[n % (2 * SLOTS)]: keys and values are decoded by different
+  // warps, and with twice as many barriers as places each barrier belongs to
+  // one of the two.  A parity wait tells only two phases apart, so a warp may
+  // wait on a barrier only after it has seen the phase before; on a barrier
+  // shared by both kinds the phase before would be the other warps' business.
+  uint64_t raw_full[2 * kMaxRaw], raw_empty[kMaxRaw], kv_full[4], kv_empty[8], s_full[2], p_full[2], o_done[2], spare;
   uint32_t tmem;
   int abort;
   int raw_bits[8];      // code width of the tile in a ring entry, 0 = a block id out of range
@@ -80,13 +87,25 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// One try of a wait, the hardware's own suspension only.
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
 // Bounded wait; on running out the CTA gives up (abort), every other wait
-// runs out in turn.
+// runs out in turn.  No sleep between tries: every wait here is short and on
+// the critical path of the next role.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* ms) {
-  if (mbar_wait(bar, parity)) return true;
+  for (unsigned i = 0; i < kTries; ++i)
+    if (phase_done(bar, parity)) return true;
   *reinterpret_cast<volatile int*>(&ms->abort) = 1;
   return false;
 }
@@ -98,58 +117,57 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Misc* 
 
 // 32 codes of one token, channels c .. c+31 of one group, as 16 half pairs in
 // the order above: fp16(code * s + z).
-__device__ __forceinline__ void decode32(int bits, bool fp8, const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
-  const __half2 k1024 = __float2half2_rn(1024.0f);
-  if (fp8) {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void decode4(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  const __half2 k1024 = __float2half2_rn(1024.0f), k16 = __float2half2_rn(0.0625f), k64 = __float2half2_rn(-64.0f);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | (4 + i) << 4));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
-        o[4 * c + i] = h2u(*reinterpret_cast<const __half2*>(&h));
-      }
-  } else if (bits == 4) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    const __half2 k16 = __float2half2_rn(0.0625f), k64 = __float2half2_rn(-64.0f);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t v = w[c] >> (8 * i);
+      const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);         // 1024 + code, exact
+      const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);      // (1024 + 16 code) / 16 - 64
+      o[4 * c + 2 * i] = h2u(__hfma2(lo, s, z));
+      o[4 * c + 2 * i + 1] = h2u(__hfma2(hi, s, z));
+    }
+}
+__device__ __forceinline__ void decode8(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
+  const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t v = w[c] >> (8 * i);
-        const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);         // 1024 + code, exact
-        const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);      // (1024 + 16 code) / 16 - 64
-        o[4 * c + 2 * i] = h2u(__hfma2(lo, s, z));
-        o[4 * c + 2 * i + 1] = h2u(__hfma2(hi, s, z));
-      }
-  } else if (bits == 8) {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
+      o[4 * c + i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), __float2half2_rn(1024.0f)), s, z));
+    }
+}
+__device__ __forceinline__ void decode2(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t v = __byte_perm(c < 2 ? a.x : a.y, 0, c & 1 ? 0x4342 : 0x4140);       // codes 0-3, codes 4-7
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
-        o[4 * c + i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), k1024), s, z));
-      }
-  } else {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t x = c < 2 ? a.x : a.y;
-      const uint32_t v = __byte_perm(x, 0, c & 1 ? 0x4342 : 0x4140);                     // codes 0-3, codes 4-7
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = 1.0f / static_cast<float>(1 << (2 * i));
-        const __half2 h = __hfma2(u2h((v & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
-                                  __float2half2_rn(-1024.0f * f));
-        o[4 * c + i] = h2u(__hfma2(h, s, z));
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float f = 1.0f / static_cast<float>(1 << (2 * i));
+      const __half2 h = __hfma2(u2h((v & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
+                                __float2half2_rn(-1024.0f * f));
+      o[4 * c + i] = h2u(__hfma2(h, s, z));
     }
   }
+}
+__device__ __forceinline__ void decode_fp8(const uint8_t* p, uint32_t (&o)[16]) {
+  const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | (4 + i) << 4));
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
+      o[4 * c + i] = h2u(*reinterpret_cast<const __half2*>(&h));
+    }
 }
 
 // Output columns 8k .. 8k+7 back in channel order.
@@ -267,14 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   const int units = w.n * (MODE == 0 ? lag : 1);          // (row tile, key tile) products
 
   if (tid == 0) {
-    for (int i = 0; i < n_raw; ++i) {
-      mbar_init(&ms->raw_full[i], 1);
-      mbar_init(&ms->raw_empty[i], kDecodeWarps);
-    }
-    for (int i = 0; i < G::SLOTS; ++i) {
-      mbar_init(&ms->kv_full[i], kDecodeWarps);
-      mbar_init(&ms->kv_empty[i], 1);
-    }
+    for (int i = 0; i < 2 * n_raw; ++i) mbar_init(&ms->raw_full[i], 1);
+    for (int i = 0; i < n_raw; ++i) mbar_init(&ms->raw_empty[i], kDecodeWarps / 2);
+    for (int i = 0; i < G::SLOTS; ++i) mbar_init(&ms->kv_full[i], kDecodeWarps / 2);
+    for (int i = 0; i < 2 * G::SLOTS; ++i) mbar_init(&ms->kv_empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->s_full[i], 1);
       mbar_init(&ms->p_full[i], MODE != 0 ? warps0 : (i == 0 ? warps0 : max(1, warps1)));
@@ -341,124 +355,159 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
   if (warp == kFeedWarp) {
     // ---- feed ------------------------------------------------------------------
-    if (lane == 0) {
-      int issued = 0;
-      bool ok = true;
-      for (int n = 0; n < 2 * w.n && ok; ++n) {
-        const int t = w.t0 + (n >> 1) * BN, e = n % n_raw;
-        const int blk = __ldg(table + t / kBlockTokens);
-        ok = wait_or_abort(&ms->raw_empty[e], ((n / n_raw) & 1) ^ 1, ms);
-        if (!ok) break;
-        uint8_t* dst = sm + kRawAt + e * raw_stride;
-        if (blk < 0 || blk >= P.n_blocks()) {
+    int issued = 0;
+    for (int n = 0; n < 2 * w.n; ++n) {
+      const int t = w.t0 + (n >> 1) * BN, e = n % n_raw;
+      const int blk = __ldg(table + t / kBlockTokens);
+      if (!warp_wait(&ms->raw_empty[e], ((n / n_raw) & 1) ^ 1, ms)) break;
+      uint64_t* full = &ms->raw_full[n % (2 * n_raw)];
+      uint8_t* dst = sm + kRawAt + e * raw_stride;
+      if (blk < 0 || blk >= P.n_blocks()) {
+        if (elect_one()) {
           raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
           ms->raw_bits[e] = 0;
-          mbar_arrive(&ms->raw_full[e]);
-        } else {
-          const int bits = P.bits_of(blk);
-          const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
-          const int64_t row = (phys * P.n_kv_heads + w.h) * kBlockTokens + t % kBlockTokens;
-          const bool key = (n & 1) == 0;
-          const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
-                                           : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
-          const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
-                                            : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
-          const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
-          ms->raw_bits[e] = bits;
-          mbar_arrive_tx(&ms->raw_full[e], cb + pb + 16);
-          bulk_g2s(dst, codes + row * (D / 8 * bits), cb, &ms->raw_full[e]);
-          if (!P.fp8) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, &ms->raw_full[e]);
-          bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16,
-                   &ms->raw_full[e]);
+          mbar_arrive(full);
         }
-        issued = n + 1;
+      } else {
+        const int bits = P.bits_of(blk);
+        const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
+        const int64_t row = (phys * P.n_kv_heads + w.h) * kBlockTokens + t % kBlockTokens;
+        const bool key = (n & 1) == 0;
+        const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
+                                         : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
+        const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
+                                          : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
+        const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
+        if (elect_one()) {
+          ms->raw_bits[e] = bits;
+          mbar_arrive_tx(full, cb + pb + 16);
+          bulk_g2s(dst, codes + row * (D / 8 * bits), cb, full);
+          if (pb > 0) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, full);
+          bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16, full);
+        }
       }
-      if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)        // let the copies in flight land
-        for (int n = max(0, issued - n_raw); n < issued; ++n) mbar_wait(&ms->raw_full[n % n_raw], (n / n_raw) & 1);
+      __syncwarp();
+      issued = n + 1;
     }
+    if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)          // let the copies in flight land
+      for (int n = max(0, issued - n_raw); n < issued; ++n) mbar_wait(&ms->raw_full[n % (2 * n_raw)], (n / (2 * n_raw)) & 1);
   } else if (warp == kMmaWarp) {
     // ---- product ---------------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kQk = mma_f16_desc(128, BN, false), kPv = mma_f16_desc(128, D, true);
-      const uint32_t q_at = smem_u32(sm), kv_at = q_at + G::kQ;
-      bool ok = true;
-      for (int u = 0; u < units + lag && ok; ++u) {
-        if (u >= lag) {                                    // O += P V of unit v
-          const int v = u - lag, buf = v % lag;
-          const int j = MODE == 0 ? v / lag : v, n = 2 * j + 1, slot = n % G::SLOTS;
-          ok = wait_or_abort(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms) && wait_or_abort(&ms->p_full[buf], (v / lag) & 1, ms);
-          if (!ok) break;
-          tc_fence_after();
-          const int oi = MODE == 2 ? 0 : buf;
-          const uint32_t at = kv_at + slot * G::kTile;
-          const bool first = MODE == 2 ? v == 0 : v < lag;
+    constexpr uint32_t kQk = mma_f16_desc(128, BN, false), kPv = mma_f16_desc(128, D, true);
+    const uint32_t q_at = smem_u32(sm), kv_at = q_at + G::kQ;
+    bool ok = true;
+    for (int u = 0; u < units + lag; ++u) {
+      if (u >= lag) {                                      // O += P V of unit v
+        const int v = u - lag, buf = v % lag;
+        const int j = MODE == 0 ? v / lag : v, n = 2 * j + 1, slot = n % G::SLOTS;
+        ok = warp_wait(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms) && warp_wait(&ms->p_full[buf], (v / lag) & 1, ms);
+        if (!ok) break;
+        tc_fence_after();
+        const int oi = MODE == 2 ? 0 : buf;
+        const uint64_t vd = smem_operand(kv_at + slot * G::kTile, BN * 128, 1024);
+        const uint32_t o = tmem + oi * 128, p = tmem + G::kSBase + buf * BN;
+        const bool first = MODE == 2 ? v == 0 : v < lag;
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            mma_ts(tmem + oi * 128, tmem + G::kSBase + buf * BN + k * 8, smem_operand(at + k * 2048, BN * 128, 1024), kPv,
-                   !first || k > 0);
+          for (int k = 0; k < BN / 16; ++k) mma_ts(o, p + k * 8, vd + k * (2048 >> 4), kPv, !first || k > 0);
           mma_commit(&ms->o_done[oi]);
-          if (MODE != 0 || v % lag == lag - 1) mma_commit(&ms->kv_empty[slot]);
+          if (MODE != 0 || buf == lag - 1) mma_commit(&ms->kv_empty[n % (2 * G::SLOTS)]);
         }
-        if (u < units) {                                   // S = Q K^T of unit u
-          const int buf = u % lag;
-          const int j = MODE == 0 ? u / lag : u, n = 2 * j, slot = n % G::SLOTS;
-          ok = wait_or_abort(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t q = q_at + (MODE == 0 ? buf * (128 * D * 2) : 0), at = kv_at + slot * G::kTile;
-          // (the product that read the weights in this buffer was issued
-          // before this one; products of one thread run in order)
+        __syncwarp();
+      }
+      if (u < units) {                                     // S = Q K^T of unit u
+        const int buf = u % lag;
+        const int j = MODE == 0 ? u / lag : u, n = 2 * j, slot = n % G::SLOTS;
+        ok = warp_wait(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = smem_operand(q_at + (MODE == 0 ? buf * (128 * D * 2) : 0), 16, 1024);
+        const uint64_t kd = smem_operand(kv_at + slot * G::kTile, 16, 1024);
+        const uint32_t s = tmem + G::kSBase + buf * BN;
+        // (the product that read the weights in this buffer was issued
+        // before this one; products of one thread run in order)
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + G::kSBase + buf * BN, smem_operand(q + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                   smem_operand(at + (k >> 2) * (BN * 128) + (k & 3) * 32, 16, 1024), kQk, k > 0);
+            mma_ss(s, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4),
+                   kQk, k > 0);
           mma_commit(&ms->s_full[buf]);
-          if (MODE != 0 || u % lag == lag - 1) mma_commit(&ms->kv_empty[slot]);
+          if (MODE != 0 || buf == lag - 1) mma_commit(&ms->kv_empty[n % (2 * G::SLOTS)]);
         }
-      }
-      if (!ok) {
-        mma_commit(&ms->spare);
-        mbar_wait(&ms->spare, 0);
+        __syncwarp();
       }
     }
-    __syncwarp();
+    if (!ok) {
+      if (elect_one()) mma_commit(&ms->spare);
+      warp_wait(&ms->spare, 0, ms);
+    }
   } else if (warp >= kDecodeWarp0) {
     // ---- decode ----------------------------------------------------------------
-    const int dw = warp - kDecodeWarp0;
+    // four warps decode the keys, four the values
+    const int dw = warp & 3, kind = (warp - kDecodeWarp0) >> 2;
     // a warp takes 8 tokens x 128 channels or 4 x 256 at a time, a lane 32
     // channels of one token; the tokens are skewed over the lanes so that both
     // the reads of codes and the swizzled writes are free of bank conflicts
     const int u = D == 128 ? lane & 3 : lane & 7;
     const int tl = D == 128 ? (((lane >> 2) & 1) + 2 * (u >> 1) + 2 * (lane >> 3)) & 7 : ((u >> 1) + (lane >> 3)) & 3;
-    bool ok = true;
-    for (int n = 0; n < 2 * w.n && ok; ++n) {
+    const bool fp8 = P.fp8;
+    for (int n = kind; n < 2 * w.n; n += 2) {
       const int e = n % n_raw, slot = n % G::SLOTS;
-      ok = warp_wait(&ms->raw_full[e], (n / n_raw) & 1, ms) && warp_wait(&ms->kv_empty[slot], ((n / G::SLOTS) & 1) ^ 1, ms);
-      if (!ok) break;
+      if (!warp_wait(&ms->raw_full[n % (2 * n_raw)], (n / (2 * n_raw)) & 1, ms)) break;
       const int bits = ms->raw_bits[e];
       const uint8_t* raw = sm + kRawAt + e * raw_stride;
       const __half2* params = reinterpret_cast<const __half2*>(raw + raw_stride - 16 - BN * (D / kGroup) * 4);
       const uint32_t* mask = reinterpret_cast<const uint32_t*>(raw + raw_stride - 16);
       const int t0 = w.t0 + (n >> 1) * BN;
       uint8_t* dst = sm + G::kQ + slot * G::kTile + (u >> 1) * (BN * 128);
+      const int before = n - G::SLOTS;                     // the tile that was in the slot
+      if (before >= 0 && !warp_wait(&ms->kv_empty[before % (2 * G::SLOTS)], (before / (2 * G::SLOTS)) & 1, ms)) break;
+      auto tile = [&](auto decode) {
+#pragma unroll 2
+        for (int it = 0; it < 4; ++it) {
+          const int t = (it * 4 + dw) * (D == 128 ? 8 : 4) + tl;
+          const int mt = (t0 + t) & 127;
+          const bool live = t0 + t < end && !((mask[mt >> 5] >> (mt & 31)) & 1u);
+          uint32_t o[16];
+          decode(t, live, o);
+          uint8_t* row = dst + (t >> 3) * 1024 + (t & 7) * 128;
 #pragma unroll
-      for (int it = 0; it < 2; ++it) {
-        const int t = (it * kDecodeWarps + dw) * (D == 128 ? 8 : 4) + tl;
-        uint32_t o[16];
-        const int mt = (t0 + t) & 127;
-        const bool live = bits != 0 && t0 + t < end && !((mask[mt >> 5] >> (mt & 31)) & 1u);
-        if (live) {
-          const __half2 sz = P.fp8 ? __half2() : params[t * (D / kGroup) + (u >> 1)];
-          decode32(bits, P.fp8, raw + (t * D + u * 32) / 8 * bits, __low2half2(sz), __high2half2(sz), o);
-        } else {
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(row + (((4 * (u & 1) + i) ^ (t & 7)) << 4)) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      };
+      // scale and zero of a slot that counts for nothing are 0, and so are its values
+      auto pair = [&](int t, bool live) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(params + t * (D / kGroup) + (u >> 1));
+        return u2h(live ? x : 0u);
+      };
+      if (bits == 0) {
+        tile([&](int, bool, uint32_t (&o)[16]) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0;
-        }
-        uint8_t* row = dst + (t >> 3) * 1024 + (t & 7) * 128;
+        });
+      } else if (fp8) {
+        tile([&](int t, bool live, uint32_t (&o)[16]) {
+          decode_fp8(raw + t * D + u * 32, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(row + (((4 * (u & 1) + i) ^ (t & 7)) << 4)) =
-              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) o[i] = live ? o[i] : 0;
+        });
+      } else if (bits == 4) {
+        tile([&](int t, bool live, uint32_t (&o)[16]) {
+          const __half2 sz = pair(t, live);
+          decode4(raw + (t * D + u * 32) / 2, __low2half2(sz), __high2half2(sz), o);
+        });
+      } else if (bits == 8) {
+        tile([&](int t, bool live, uint32_t (&o)[16]) {
+          const __half2 sz = pair(t, live);
+          decode8(raw + t * D + u * 32, __low2half2(sz), __high2half2(sz), o);
+        });
+      } else {
+        tile([&](int t, bool live, uint32_t (&o)[16]) {
+          const __half2 sz = pair(t, live);
+          decode2(raw + (t * D + u * 32) / 4, __low2half2(sz), __high2half2(sz), o);
+        });
       }
       fence_async_shared();
       __syncwarp();
@@ -487,16 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const uint32_t phase = (MODE == 2 ? k >> 1 : k) & 1;
       const int t0 = w.t0 + (MODE == 1 ? 2 * k + st : k) * BN;
       const uint32_t s_at = tmem + lanes + G::kSBase + buf * BN;
-      uint32_t gone[BN / 32];
-#pragma unroll
-      for (int c = 0; c < BN / 32; ++c) gone[c] = 0;
       const int blk = __ldg(table + t0 / kBlockTokens);
       const bool bad = blk < 0 || blk >= P.n_blocks();
+      const uint32_t* mw = P.mask + static_cast<int64_t>(blk) * kMaskWords + (t0 % kBlockTokens) / 32;
       uint32_t any = 0;
       if (!bad) {
-        const uint32_t* mw = P.mask + static_cast<int64_t>(blk) * kMaskWords + (t0 % kBlockTokens) / 32;
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) any |= gone[c] = __ldg(mw + c);
+        for (int c = 0; c < BN / 32; ++c) any |= __ldg(mw + c);
       }
       const int hi = pos - t0;                             // last column the row sees
       const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
@@ -506,28 +552,37 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if (!ok) break;
       tc_fence_after();
 
-      uint32_t x[32];
-      // logits of columns 32c .. 32c+31, with the mask applied
-      auto load = [&](int c) {
-        tmem_ld32(s_at + 32 * c, x);
-        tmem_wait_ld();
-        if (!plain) {
+      if (!plain) {          // write the mask into the logits
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(s_at + 32 * c, x);
+          tmem_wait_ld();
           const int h1 = hi - 32 * c, l1 = lo - 32 * c;
           uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
           seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
+          const uint32_t away = bad ? 0u : __ldg(mw + c);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float y = (gone[c] >> i) & 1u ? sent : __uint_as_float(x[i]);
+            const float y = (away >> i) & 1u ? sent : __uint_as_float(x[i]);
             x[i] = __float_as_uint((seen >> i) & 1u ? y : -INFINITY);
           }
+          tmem_st32(s_at + 32 * c, x);
         }
-      };
+        tmem_wait_st();
+      }
       float mx = -INFINITY;
+      {
+        uint32_t x[2][32];
+        tmem_ld32(s_at, x[0]);
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
-        load(c);
+        for (int c = 0; c < BN / 32; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < BN / 32) tmem_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          for (int i = 0; i < 32; i += 2)
+            mx = max3(mx, __uint_as_float(x[c & 1][i]), __uint_as_float(x[c & 1][i + 1]));
+        }
       }
       const float top = fmaxf(m, mx * rs);
       if (k == 0) {
@@ -542,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         m = top;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
           tmem_ld32(o_at + 32 * c, x);
           tmem_wait_ld();
 #pragma unroll
@@ -551,22 +607,28 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         tmem_wait_st();
       }
       const float off = kShift - (m == -INFINITY ? 0.0f : m);
-      float sum0 = 0.0f, sum1 = 0.0f;
+      float2 sum = make_float2(0.0f, 0.0f);
+      const float2 rs2 = make_float2(rs, rs), off2 = make_float2(off, off);
+      {
+        uint32_t x[2][16];
+        tmem_ld16(s_at, x[0]);
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
-        load(c);
-        uint32_t p[16];
+        for (int c = 0; c < BN / 16; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < BN / 16) tmem_ld16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
+          uint32_t p[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), rs, off));
-          const float p1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), rs, off));
-          sum0 += p0;
-          sum1 += p1;
-          p[i] = h2u(__floats2half2_rn(p0, p1));
+          for (int i = 0; i < 8; ++i) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c & 1][2 * i]), __uint_as_float(x[c & 1][2 * i + 1])),
+                                        rs2, off2);
+            const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            sum = __fadd2_rn(sum, q);
+            p[i] = h2u(__floats2half2_rn(q.x, q.y));
+          }
+          tmem_st8(s_at + 8 * c, p);
         }
-        tmem_st16(s_at + 16 * c, p);
       }
-      l += sum0 + sum1;
+      l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
