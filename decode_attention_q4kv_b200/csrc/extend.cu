@@ -115,59 +115,96 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Misc* 
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, ms));
 }
 
-// 32 codes of one token, channels c .. c+31 of one group, as 16 half pairs in
-// the order above: fp16(code * s + z).
-__device__ __forceinline__ void decode4(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// A decoding lane's place: its first token in the tile and its 32-channel
+// unit; its four tokens lie step() apart.
+struct Lane {
+  int t, u;
+  static constexpr __host__ __device__ int step(int d) { return d == 128 ? 32 : 16; }
+};
+
+// 8 codes as 4 half pairs in the order above: fp16(code * s + z), one rounding.
+// 0x64xx is 1024 + xx in fp16: a mask and an or give codes exactly, less 1024.
+__device__ __forceinline__ void codes4(uint32_t w, __half2 s, __half2 z, uint32_t* o) {
   const __half2 k1024 = __float2half2_rn(1024.0f), k16 = __float2half2_rn(0.0625f), k64 = __float2half2_rn(-64.0f);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t v = w[c] >> (8 * i);
-      const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);         // 1024 + code, exact
-      const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);      // (1024 + 16 code) / 16 - 64
-      o[4 * c + 2 * i] = h2u(__hfma2(lo, s, z));
-      o[4 * c + 2 * i + 1] = h2u(__hfma2(hi, s, z));
-    }
-}
-__device__ __forceinline__ void decode8(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
-  const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
-      o[4 * c + i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), __float2half2_rn(1024.0f)), s, z));
-    }
-}
-__device__ __forceinline__ void decode2(const uint8_t* p, __half2 s, __half2 z, uint32_t (&o)[16]) {
-  const uint2 a = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t v = __byte_perm(c < 2 ? a.x : a.y, 0, c & 1 ? 0x4342 : 0x4140);       // codes 0-3, codes 4-7
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = 1.0f / static_cast<float>(1 << (2 * i));
-      const __half2 h = __hfma2(u2h((v & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
-                                __float2half2_rn(-1024.0f * f));
-      o[4 * c + i] = h2u(__hfma2(h, s, z));
-    }
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t v = w >> (8 * i);
+    const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);
+    const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);   // (1024 + 16 code) / 16 - 64
+    o[2 * i] = h2u(__hfma2(lo, s, z));
+    o[2 * i + 1] = h2u(__hfma2(hi, s, z));
   }
 }
-__device__ __forceinline__ void decode_fp8(const uint8_t* p, uint32_t (&o)[16]) {
-  const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void codes8(uint32_t w0, uint32_t w1, __half2 s, __half2 z, uint32_t* o) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = __byte_perm(w0, w1, static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
+    o[i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), __float2half2_rn(1024.0f)), s, z));
+  }
+}
+__device__ __forceinline__ void codes2(uint32_t w16, __half2 s, __half2 z, uint32_t* o) {   // codes 0-3, codes 4-7 in halves
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = __byte_perm(w[2 * c], w[2 * c + 1], static_cast<uint32_t>(i | (4 + i) << 4));
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
-      o[4 * c + i] = h2u(*reinterpret_cast<const __half2*>(&h));
+  for (int i = 0; i < 4; ++i) {
+    const float f = 1.0f / static_cast<float>(1 << (2 * i));
+    const __half2 h = __hfma2(u2h((w16 & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
+                              __float2half2_rn(-1024.0f * f));
+    o[i] = h2u(__hfma2(h, s, z));
+  }
+}
+__device__ __forceinline__ void codes_fp8(uint32_t w0, uint32_t w1, bool live, uint32_t* o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = __byte_perm(w0, w1, static_cast<uint32_t>(i | (4 + i) << 4));
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xFFFFu), __NV_E4M3);
+    o[i] = live ? h2u(*reinterpret_cast<const __half2*>(&h)) : 0u;
+  }
+}
+
+// The lane's four tokens of a tile, 32 channels each.  The loads come first so
+// that their latencies overlap.  A token that does not count takes scale and
+// zero 0 (whatever its own are), so its values are 0.  BITS 0: E4M3 bytes.
+template <int D, int BITS>
+__device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* params, const Lane& ln, uint32_t live,
+                                            uint8_t* dst) {
+  constexpr int W = BITS == 0 ? 8 : BITS;              // words of 32 codes
+  constexpr int TS = Lane::step(D);
+  constexpr int ROW = D / 8 * W;                       // bytes of a token
+  const uint8_t* src = raw + ln.t * ROW + ln.u * 4 * W;
+#pragma unroll 1
+  for (int it = 0; it < 4; ++it) {
+    const uint8_t* p = src + it * TS * ROW;
+    uint32_t w[W];
+    if (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[q];
+        w[4 * q] = x.x;
+        w[4 * q + 1] = x.y;
+        w[(4 * q + 2) % W] = x.z;
+        w[(4 * q + 3) % W] = x.w;
+      }
     }
+    const bool on = (live >> it) & 1u;
+    uint32_t sz = 0;
+    if (BITS != 0) sz = *reinterpret_cast<const uint32_t*>(params + ((ln.t + it * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
+    const __half2 q = u2h(on ? sz : 0u);
+    const __half2 s = __low2half2(q), z = __high2half2(q);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[4];
+      if (BITS == 0) codes_fp8(w[(2 * c) % W], w[(2 * c + 1) % W], on, o);
+      else if (BITS == 8) codes8(w[(2 * c) % W], w[(2 * c + 1) % W], s, z, o);
+      else if (BITS == 4) codes4(w[c % W], s, z, o);
+      else codes2(__byte_perm(w[(c >> 1) % W], 0, c & 1 ? 0x4342 : 0x4140), s, z, o);
+      // (the lane's tokens are the same modulo 8)
+      *reinterpret_cast<uint4*>(dst + it * (TS / 8) * 1024 + (((4 * (ln.u & 1) + c) ^ (ln.t & 7)) << 4)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 // Output columns 8k .. 8k+7 back in channel order.
@@ -355,12 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
   if (warp == kFeedWarp) {
     // ---- feed ------------------------------------------------------------------
-    int issued = 0;
+    int issued = 0, e = -1, f = -1;
+    uint32_t lap = 0;                                      // parity of n / n_raw
     for (int n = 0; n < 2 * w.n; ++n) {
-      const int t = w.t0 + (n >> 1) * BN, e = n % n_raw;
+      const int t = w.t0 + (n >> 1) * BN;
       const int blk = __ldg(table + t / kBlockTokens);
-      if (!warp_wait(&ms->raw_empty[e], ((n / n_raw) & 1) ^ 1, ms)) break;
-      uint64_t* full = &ms->raw_full[n % (2 * n_raw)];
+      if (++e == n_raw) e = 0, lap ^= 1;
+      if (++f == 2 * n_raw) f = 0;
+      if (!warp_wait(&ms->raw_empty[e], lap ^ 1, ms)) break;
+      uint64_t* full = &ms->raw_full[f];
       uint8_t* dst = sm + kRawAt + e * raw_stride;
       if (blk < 0 || blk >= P.n_blocks()) {
         if (elect_one()) {
@@ -448,73 +488,48 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     // a warp takes 8 tokens x 128 channels or 4 x 256 at a time, a lane 32
     // channels of one token; the tokens are skewed over the lanes so that both
     // the reads of codes and the swizzled writes are free of bank conflicts
-    const int u = D == 128 ? lane & 3 : lane & 7;
-    const int tl = D == 128 ? (((lane >> 2) & 1) + 2 * (u >> 1) + 2 * (lane >> 3)) & 7 : ((u >> 1) + (lane >> 3)) & 3;
-    const bool fp8 = P.fp8;
+    Lane ln;
+    ln.u = D == 128 ? lane & 3 : lane & 7;
+    ln.t = D == 128 ? dw * 8 + ((((lane >> 2) & 1) + 2 * (ln.u >> 1) + 2 * (lane >> 3)) & 7)
+                    : dw * 4 + (((ln.u >> 1) + (lane >> 3)) & 3);
+    const uint32_t dst0 = (ln.u >> 1) * (BN * 128) + (ln.t >> 3) * 1024 + (ln.t & 7) * 128;
+    int e = kind, f = kind;                                // n % n_raw, n % (2 n_raw)
+    uint32_t lap = 0;                                      // parity of n / (2 n_raw)
     for (int n = kind; n < 2 * w.n; n += 2) {
-      const int e = n % n_raw, slot = n % G::SLOTS;
-      if (!warp_wait(&ms->raw_full[n % (2 * n_raw)], (n / (2 * n_raw)) & 1, ms)) break;
+      const int slot = n % G::SLOTS;
+      if (!warp_wait(&ms->raw_full[f], lap, ms)) break;
       const int bits = ms->raw_bits[e];
       const uint8_t* raw = sm + kRawAt + e * raw_stride;
-      const __half2* params = reinterpret_cast<const __half2*>(raw + raw_stride - 16 - BN * (D / kGroup) * 4);
-      const uint32_t* mask = reinterpret_cast<const uint32_t*>(raw + raw_stride - 16);
+      const uint8_t* params = raw + raw_stride - 16 - BN * (D / kGroup) * 4;
       const int t0 = w.t0 + (n >> 1) * BN;
-      uint8_t* dst = sm + G::kQ + slot * G::kTile + (u >> 1) * (BN * 128);
+      // which of the lane's four tokens count
+      uint32_t live = 0;
+      {
+        const uint4 m = *reinterpret_cast<const uint4*>(raw + raw_stride - 16);
+        const uint32_t m0 = D == 128 || (t0 & 64) == 0 ? m.x : m.z, m1 = D == 128 || (t0 & 64) == 0 ? m.y : m.w;
+        const uint32_t word[4] = {m0, D == 128 ? m1 : m0, D == 128 ? m.z : m1, D == 128 ? m.w : m1};
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int bit = D == 128 ? ln.t : ln.t + 16 * (it & 1);
+          if (t0 + ln.t + it * Lane::step(D) < end && !((word[it] >> bit) & 1u)) live |= 1u << it;
+        }
+      }
+      if (bits == 0) live = 0;
       const int before = n - G::SLOTS;                     // the tile that was in the slot
       if (before >= 0 && !warp_wait(&ms->kv_empty[before % (2 * G::SLOTS)], (before / (2 * G::SLOTS)) & 1, ms)) break;
-      auto tile = [&](auto decode) {
-#pragma unroll 2
-        for (int it = 0; it < 4; ++it) {
-          const int t = (it * 4 + dw) * (D == 128 ? 8 : 4) + tl;
-          const int mt = (t0 + t) & 127;
-          const bool live = t0 + t < end && !((mask[mt >> 5] >> (mt & 31)) & 1u);
-          uint32_t o[16];
-          decode(t, live, o);
-          uint8_t* row = dst + (t >> 3) * 1024 + (t & 7) * 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(row + (((4 * (u & 1) + i) ^ (t & 7)) << 4)) =
-                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
-      };
-      // scale and zero of a slot that counts for nothing are 0, and so are its values
-      auto pair = [&](int t, bool live) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(params + t * (D / kGroup) + (u >> 1));
-        return u2h(live ? x : 0u);
-      };
-      if (bits == 0) {
-        tile([&](int, bool, uint32_t (&o)[16]) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0;
-        });
-      } else if (fp8) {
-        tile([&](int t, bool live, uint32_t (&o)[16]) {
-          decode_fp8(raw + t * D + u * 32, o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = live ? o[i] : 0;
-        });
-      } else if (bits == 4) {
-        tile([&](int t, bool live, uint32_t (&o)[16]) {
-          const __half2 sz = pair(t, live);
-          decode4(raw + (t * D + u * 32) / 2, __low2half2(sz), __high2half2(sz), o);
-        });
-      } else if (bits == 8) {
-        tile([&](int t, bool live, uint32_t (&o)[16]) {
-          const __half2 sz = pair(t, live);
-          decode8(raw + t * D + u * 32, __low2half2(sz), __high2half2(sz), o);
-        });
-      } else {
-        tile([&](int t, bool live, uint32_t (&o)[16]) {
-          const __half2 sz = pair(t, live);
-          decode2(raw + (t * D + u * 32) / 4, __low2half2(sz), __high2half2(sz), o);
-        });
-      }
+      uint8_t* dst = sm + G::kQ + slot * G::kTile + dst0;
+      if (P.fp8) decode_tile<D, 0>(raw, params, ln, live, dst);
+      else if (bits == 8) decode_tile<D, 8>(raw, params, ln, live, dst);
+      else if (bits == 2) decode_tile<D, 2>(raw, params, ln, live, dst);
+      else decode_tile<D, 4>(raw, params, ln, live, dst);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ms->raw_empty[e]);
         mbar_arrive(&ms->kv_full[slot]);
       }
+      if ((e += 2) >= n_raw) e -= n_raw;
+      if ((f += 2) >= 2 * n_raw) f -= 2 * n_raw, lap ^= 1;
     }
   } else if ((MODE == 2 ? warp < 4 : true) && (warp & 3) < (warp < 4 ? warps0 : warps1)) {
     // ---- softmax ---------------------------------------------------------------
@@ -573,15 +588,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       }
       float mx = -INFINITY;
       {
-        uint32_t x[2][32];
-        tmem_ld32(s_at, x[0]);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(s_at + 32 * c, x);
           tmem_wait_ld();
-          if (c + 1 < BN / 32) tmem_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+          float m0 = mx, m1 = __uint_as_float(x[31]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx = max3(mx, __uint_as_float(x[c & 1][i]), __uint_as_float(x[c & 1][i + 1]));
+          for (int i = 0; i < 16; i += 2) {
+            m0 = max3(m0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            m1 = max3(m1, __uint_as_float(x[i + 16]), __uint_as_float(x[i + 17]));
+          }
+          mx = fmaxf(m0, m1);
         }
       }
       const float top = fmaxf(m, mx * rs);
@@ -610,22 +628,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       float2 sum = make_float2(0.0f, 0.0f);
       const float2 rs2 = make_float2(rs, rs), off2 = make_float2(off, off);
       {
-        uint32_t x[2][16];
-        tmem_ld16(s_at, x[0]);
-#pragma unroll
-        for (int c = 0; c < BN / 16; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t x[32], p[16];
+          tmem_ld32(s_at + 32 * c, x);
           tmem_wait_ld();
-          if (c + 1 < BN / 16) tmem_ld16(s_at + 16 * (c + 1), x[(c + 1) & 1]);
-          uint32_t p[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c & 1][2 * i]), __uint_as_float(x[c & 1][2 * i + 1])),
-                                        rs2, off2);
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rs2, off2);
             const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum = __fadd2_rn(sum, q);
             p[i] = h2u(__floats2half2_rn(q.x, q.y));
           }
-          tmem_st8(s_at + 8 * c, p);
+          tmem_st16(s_at + 16 * c, p);
         }
       }
       l += sum.x + sum.y;
