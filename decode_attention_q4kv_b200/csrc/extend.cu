@@ -87,6 +87,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^x = 2^n 2^f, n = rint(x), |f| <= 1/2, 2^f by the cubic of least relative
+// error on that interval (Remez exchange; 7.5e-5 = 2^-13.7, below the 2^-11 of
+// the weights' rounding to fp16).  x is held above -126, where the result no
+// longer counts.
+__device__ __forceinline__ float2 exp2_poly(float2 x) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it leaves n in the low bits
+  x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
+  const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
+  const float2 f = __fadd2_rn(x, __ffma2_rn(t, make_float2(-1.0f, -1.0f), make_float2(kMagic, kMagic)));
+  float2 p = __ffma2_rn(f, make_float2(0x1.c3f760p-5f, 0x1.c3f760p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
+  p = __ffma2_rn(p, f, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
+  p = __ffma2_rn(p, f, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
 // One try of a wait, the hardware's own suspension only.
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -171,38 +186,44 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
   constexpr int ROW = D / 8 * W;                       // bytes of a token
   const uint8_t* src = raw + ln.t * ROW + ln.u * 4 * W;
 #pragma unroll 1
-  for (int it = 0; it < 4; ++it) {
-    const uint8_t* p = src + it * TS * ROW;
-    uint32_t w[W];
-    if (W == 2) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
-      w[0] = x.x;
-      w[1] = x.y;
-    } else {
+  for (int i2 = 0; i2 < 4; i2 += 2) {
+    uint32_t w[2][W], sz[2] = {0u, 0u};
 #pragma unroll
-      for (int q = 0; q < W / 4; ++q) {
-        const uint4 x = reinterpret_cast<const uint4*>(p)[q];
-        w[4 * q] = x.x;
-        w[4 * q + 1] = x.y;
-        w[(4 * q + 2) % W] = x.z;
-        w[(4 * q + 3) % W] = x.w;
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* p = src + (i2 + i) * TS * ROW;
+      if (W == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[i][0] = x.x;
+        w[i][1] = x.y;
+      } else {
+#pragma unroll
+        for (int q = 0; q < W / 4; ++q) {
+          const uint4 x = reinterpret_cast<const uint4*>(p)[q];
+          w[i][4 * q] = x.x;
+          w[i][4 * q + 1] = x.y;
+          w[i][(4 * q + 2) % W] = x.z;
+          w[i][(4 * q + 3) % W] = x.w;
+        }
       }
+      if (BITS != 0)
+        sz[i] = *reinterpret_cast<const uint32_t*>(params + ((ln.t + (i2 + i) * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
     }
-    const bool on = (live >> it) & 1u;
-    uint32_t sz = 0;
-    if (BITS != 0) sz = *reinterpret_cast<const uint32_t*>(params + ((ln.t + it * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
-    const __half2 q = u2h(on ? sz : 0u);
-    const __half2 s = __low2half2(q), z = __high2half2(q);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[4];
-      if (BITS == 0) codes_fp8(w[(2 * c) % W], w[(2 * c + 1) % W], on, o);
-      else if (BITS == 8) codes8(w[(2 * c) % W], w[(2 * c + 1) % W], s, z, o);
-      else if (BITS == 4) codes4(w[c % W], s, z, o);
-      else codes2(__byte_perm(w[(c >> 1) % W], 0, c & 1 ? 0x4342 : 0x4140), s, z, o);
-      // (the lane's tokens are the same modulo 8)
-      *reinterpret_cast<uint4*>(dst + it * (TS / 8) * 1024 + (((4 * (ln.u & 1) + c) ^ (ln.t & 7)) << 4)) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < 2; ++i) {
+      const bool on = (live >> (i2 + i)) & 1u;
+      const __half2 q = u2h(on ? sz[i] : 0u);
+      const __half2 s = __low2half2(q), z = __high2half2(q);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[4];
+        if (BITS == 0) codes_fp8(w[i][(2 * c) % W], w[i][(2 * c + 1) % W], on, o);
+        else if (BITS == 8) codes8(w[i][(2 * c) % W], w[i][(2 * c + 1) % W], s, z, o);
+        else if (BITS == 4) codes4(w[i][c % W], s, z, o);
+        else codes2(__byte_perm(w[i][(c >> 1) % W], 0, c & 1 ? 0x4342 : 0x4140), s, z, o);
+        // (the lane's tokens are the same modulo 8)
+        *reinterpret_cast<uint4*>(dst + (i2 + i) * (TS / 8) * 1024 + (((4 * (ln.u & 1) + c) ^ (ln.t & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
 }
@@ -450,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k) mma_ts(o, p + k * 8, vd + k * (2048 >> 4), kPv, !first || k > 0);
-          mma_commit(&ms->o_done[oi]);
+          mma_commit(&ms->o_done[buf]);
           if (MODE != 0 || buf == lag - 1) mma_commit(&ms->kv_empty[n % (2 * G::SLOTS)]);
         }
         __syncwarp();
@@ -545,6 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     const int steps = MODE == 1 ? (w.n - st + 1) / 2 : w.n;
     float m = -INFINITY, l = 0.0f;
     bool poison = false, ok = true;
+    // Wait for the k-th product into the accumulator.  With two logit buffers
+    // on one accumulator the softmax can be a product further than in the
+    // other modes, so each buffer has its barrier.
+    auto product_done = [&](int k) {
+      return warp_wait(&ms->o_done[MODE == 2 ? k & 1 : st], (MODE == 2 ? k >> 1 : k) & 1, ms);
+    };
 
     for (int k = 0; k < steps; ++k) {
       const int buf = MODE == 2 ? k & 1 : st;
@@ -589,15 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       float mx = -INFINITY;
       {
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32(s_at + 32 * c, x);
+        for (int c = 0; c < BN / 64; ++c) {
+          uint32_t x[32], y[32];
+          tmem_ld32(s_at + 64 * c, x);
+          tmem_ld32(s_at + 64 * c + 32, y);
           tmem_wait_ld();
-          float m0 = mx, m1 = __uint_as_float(x[31]);
+          float m0 = mx, m1 = __uint_as_float(y[31]);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < 32; i += 2) {
             m0 = max3(m0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            m1 = max3(m1, __uint_as_float(x[i + 16]), __uint_as_float(x[i + 17]));
+            m1 = max3(m1, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
           }
           mx = fmaxf(m0, m1);
         }
@@ -607,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         m = top;
       } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
         // move the maximum: rescale the accumulator and the sum
-        ok = warp_wait(&ms->o_done[MODE == 2 ? 0 : st], (k - 1) & 1, ms);
+        ok = product_done(k - 1);
         if (!ok) break;
         tc_fence_after();
         const float f = top == -INFINITY ? 1.0f : exp2_fast(m - top);
@@ -636,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rs2, off2);
-            const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            // a quarter of the exponentials on the FMA pipe: the special-
+            // function unit (16 a clock) is what the tile waits for otherwise
+            const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum = __fadd2_rn(sum, q);
             p[i] = h2u(__floats2half2_rn(q.x, q.y));
           }
@@ -651,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
 
     // ---- result ----------------------------------------------------------------
-    if (ok && steps > 0) ok = warp_wait(&ms->o_done[MODE == 2 ? 0 : st], (steps - 1) & 1, ms);
+    if (ok && steps > 0) ok = product_done(steps - 1);
     tc_fence_after();
     const int i = r / w.g, head = w.h * w.g + r % w.g;
     const int64_t row = (static_cast<int64_t>(w.b) * w.T + i) * hq + head;
