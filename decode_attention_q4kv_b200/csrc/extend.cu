@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if (elect_one()) mma_commit(&ms->spare);
       warp_wait(&ms->spare, 0, ms);
     }
-  } else if (warp >= kDecodeWarp0) {
+  } else if (warp >= kDecodeWarp0 && warp < kMmaWarp) {
     // ---- decode ----------------------------------------------------------------
     // four warps decode the keys, four the values
     const int dw = warp & 3, kind = (warp - kDecodeWarp0) >> 2;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if ((e += 2) >= n_raw) e -= n_raw;
       if ((f += 2) >= 2 * n_raw) f -= 2 * n_raw, lap ^= 1;
     }
-  } else if ((MODE == 2 ? warp < 4 : true) && (warp & 3) < (warp < 4 ? warps0 : warps1)) {
+  } else if (warp < (MODE == 2 ? 4 : 8) && (warp & 3) < (warp < 4 ? warps0 : warps1)) {
     // ---- softmax ---------------------------------------------------------------
     const int st = MODE == 2 ? 0 : warp >> 2;              // stream
     const int local = (MODE == 0 ? st * 128 : 0) + (warp & 3) * 32 + lane;
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         for (int c = 0; c < BN / 32; ++c) {
           uint32_t x[32];
           tmem_ld32(s_at + 32 * c, x);
-          tmem_wait_ld();
+          tmem_wait_ld(x);
           const int h1 = hi - 32 * c, l1 = lo - 32 * c;
           uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
           seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
@@ -613,67 +613,73 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         }
         tmem_wait_st();
       }
-      float mx = -INFINITY;
-      {
+      // weights of 32 columns at a time
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      float off = kShift - (m == -INFINITY ? 0.0f : m);
+      const float2 rs2 = make_float2(rs, rs);
 #pragma unroll 1
-        for (int c = 0; c < BN / 64; ++c) {
-          uint32_t x[32], y[32];
-          tmem_ld32(s_at + 64 * c, x);
-          tmem_ld32(s_at + 64 * c + 32, y);
-          tmem_wait_ld();
-          float m0 = mx, m1 = __uint_as_float(y[31]);
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t x[32];
+        tmem_ld32(s_at + 32 * c, x);
+        tmem_wait_ld(x);
+        float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            m0 = max3(m0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            m1 = max3(m1, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+        for (int i = 2; i < 30; i += 4) {
+          mx[0] = max3(mx[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          mx[1] = max3(mx[1], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+        }
+        const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * rs;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          // Move the reference: it stays a whole number, so everything scaled
+          // by it scales by a power of two.
+          const float to = ceilf(fmaxf(m, top));
+          const float f = to == -INFINITY ? 1.0f : __int_as_float((static_cast<int>(fmaxf(m - to, -127.0f)) + 127) << 23);
+          m = to;
+          off = kShift - (m == -INFINITY ? 0.0f : m);
+          if (k > 0 || c > 0) {
+            l *= f;
+            sum[0] = make_float2(sum[0].x * f, sum[0].y * f);
+            sum[1] = make_float2(sum[1].x * f, sum[1].y * f);
+            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+            for (int e = 0; e < c; ++e) {                  // weights of this tile so far
+              uint32_t p[16];
+              tmem_ld16(s_at + 16 * e, p);
+              tmem_wait_ld(p);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i] = h2u(__hmul2(u2h(p[i]), f2));
+              tmem_st16(s_at + 16 * e, p);
+            }
+            if (k > 0) {
+              ok = product_done(k - 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int e = 0; ok && e < D / 16; ++e) {
+                uint32_t o[16];
+                tmem_ld16(o_at + 16 * e, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16(o_at + 16 * e, o);
+              }
+            }
           }
-          mx = fmaxf(m0, m1);
         }
-      }
-      const float top = fmaxf(m, mx * rs);
-      if (k == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, top > m + kLazy)) {
-        // move the maximum: rescale the accumulator and the sum
-        ok = product_done(k - 1);
-        if (!ok) break;
-        tc_fence_after();
-        const float f = top == -INFINITY ? 1.0f : exp2_fast(m - top);
-        l *= f;
-        m = top;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32(o_at + 32 * c, x);
-          tmem_wait_ld();
+        const float2 off2 = make_float2(off, off);
+        uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-          tmem_st32(o_at + 32 * c, x);
+        for (int i = 0; i < 16; ++i) {
+          const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rs2, off2);
+          // a quarter of the exponentials on the FMA pipe: the special-
+          // function unit (16 a clock) is what the tile waits for otherwise
+          const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
+          sum[i & 1] = __fadd2_rn(sum[i & 1], q);
+          p[i] = h2u(__floats2half2_rn(q.x, q.y));
         }
-        tmem_wait_st();
+        tmem_st16(s_at + 16 * c, p);
       }
-      const float off = kShift - (m == -INFINITY ? 0.0f : m);
-      float2 sum = make_float2(0.0f, 0.0f);
-      const float2 rs2 = make_float2(rs, rs), off2 = make_float2(off, off);
-      {
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t x[32], p[16];
-          tmem_ld32(s_at + 32 * c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rs2, off2);
-            // a quarter of the exponentials on the FMA pipe: the special-
-            // function unit (16 a clock) is what the tile waits for otherwise
-            const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
-            sum = __fadd2_rn(sum, q);
-            p[i] = h2u(__floats2half2_rn(q.x, q.y));
-          }
-          tmem_st16(s_at + 16 * c, p);
-        }
-      }
-      l += sum.x + sum.y;
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -695,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         uint32_t x[32];
         float y[32];
         tmem_ld32(o_at + 32 * c, x);
-        tmem_wait_ld();
+        tmem_wait_ld(x);
         channel_order(x, f, y);
         if (partials == 1 && !fine) {
 #pragma unroll
