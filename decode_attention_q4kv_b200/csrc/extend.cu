@@ -6,16 +6,22 @@
 // their keys in tiles, S = Q K^T and O += P V on the tensor cores (fp16
 // operands, fp32 accumulators in tensor memory).
 //
-// Warp roles (18 warps):
-//   feed     one thread copies each tile's packed codes, scales and mask into a
-//            ring in shared memory (bulk copies)
+// Warp roles (20 warps, the last two idle):
+//   softmax  two groups of four warps, one row per thread: maximum, weights, sum
+//            of 64 columns at a time.  The weights go back into the tensor memory
+//            that held the logits, and are the A operand of the second product.
 //   decode   four warps turn the keys' codes into fp16, four the values', in the
 //            layout the tensor cores read (rows of 128 bytes, 128-byte swizzle);
 //            remapped slots and slots past the end become zeros
 //   product  one thread issues the matrix products
-//   softmax  eight warps, one row per thread: maximum, weights, sum.  The
-//            weights go back into the tensor memory that held the logits, and
-//            are the A operand of the second product.
+//   feed     one thread copies each tile's packed codes, scales and mask into a
+//            ring in shared memory (bulk copies)
+// A softmax group has two buffers of 64 logit columns: while it works on one, the
+// product of the weights before and the logits after run.  (With one buffer of
+// 128 columns the group waited for both products and every hand-over in turn;
+// leaving out the products and the exponentials then saved only 40 % of the
+// time.)
+//
 // Within 8 channels the decoded order is 0 4 1 5 2 6 3 7 (what one mask and one
 // subtraction per pair of codes leave); q is stored in the same order and the
 // output's columns are put back when they are written.
@@ -36,51 +42,54 @@ namespace q4kv {
 namespace {
 
 constexpr int kDecodeWarp0 = 8, kMmaWarp = 16, kFeedWarp = 17;
-constexpr int kThreads = 18 * 32;
-constexpr int kDecodeWarps = 8;
+constexpr int kThreads = 20 * 32;
+// Registers: 96 a thread at launch, shared out anew by role.
+constexpr int kRegs = 96, kSoftRegs = 120, kDecodeRegs = 80, kOtherRegs = 80;
+static_assert(8 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 20 * kRegs, "register shares");
+constexpr int kCols = 64;        // logit columns of a softmax step
+constexpr int kSlots = 4;        // decoded tiles
+constexpr uint32_t kTile = 32768;// bytes of a decoded tile
+constexpr uint32_t kSBase = 256; // tensor-memory columns: accumulators from 0, logits from here
+constexpr int kMaxRaw = 7;
 constexpr float kShift = 6.0f;   // weights are stored times 2^6
 constexpr float kLazy = 8.0f;    // growth of the maximum (log2) that moves it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 
-// MODE 0: D = 128, two row tiles of 128, each with its softmax warps.
-// MODE 1: D = 128, one row tile; the two sets of softmax warps take alternate
-//         key tiles with their own accumulators (two partial results).
-// MODE 2: D = 256, one row tile, key tiles of 64 with two logit buffers.
+// MODE 0: D = 128, two row tiles of 128, a softmax group each.
+// MODE 1: D = 128, one row tile; the two softmax groups take alternate key tiles
+//         with their own accumulators (two partial results).
+// MODE 2: D = 256, one row tile, one softmax group.
 template <int MODE>
 struct Geo {
   static constexpr int D = MODE == 2 ? 256 : 128;
   static constexpr int BN = MODE == 2 ? 64 : 128;      // tokens of a key tile
+  static constexpr int STEPS = BN / kCols;             // softmax steps of a key tile
   static constexpr int QT = MODE == 0 ? 2 : 1;         // row tiles
   static constexpr int STREAMS = MODE == 1 ? 2 : 1;    // partial results of a row
   static constexpr int R = 128 * QT;
-  static constexpr int SLOTS = MODE == 1 ? 4 : 3;      // decoded tiles
-  static constexpr uint32_t kTile = BN * D * 2;        // bytes of a decoded tile
   static constexpr uint32_t kQ = QT * 128 * D * 2;
-  static constexpr uint32_t kSBase = 256;              // tensor-memory columns: O from 0, S from here
+  static constexpr uint32_t kRawAt = kQ + kSlots * kTile;
+  static constexpr uint32_t kRawRing = MODE == 1 ? 67616 : 34848;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
+  static constexpr uint32_t kMiscAt = kRawAt + kRawRing;
 };
-constexpr uint32_t kRawRing = 65536;
-constexpr uint32_t kRawAt = 163840;                    // Q and the decoded tiles fill this in every mode
-constexpr uint32_t kMiscAt = kRawAt + kRawRing;
-constexpr uint32_t kSmem = kMiscAt + 2048;
-static_assert(Geo<0>::kQ + Geo<0>::SLOTS * Geo<0>::kTile == kRawAt && Geo<1>::kQ + Geo<1>::SLOTS * Geo<1>::kTile == kRawAt &&
-              Geo<2>::kQ + Geo<2>::SLOTS * Geo<2>::kTile == kRawAt, "shared memory layout");
-constexpr int kMaxRaw = 7;
 
 struct Misc {
   // Copy n (keys and values in turn) completes raw_full[n % (2 * entries)] and
-  // frees kv_empty[n % (2 * SLOTS)]: keys and values are decoded by different
+  // frees kv_empty[n % (2 * kSlots)]: keys and values are decoded by different
   // warps, and with twice as many barriers as places each barrier belongs to
   // one of the two.  A parity wait tells only two phases apart, so a warp may
   // wait on a barrier only after it has seen the phase before; on a barrier
   // shared by both kinds the phase before would be the other warps' business.
-  uint64_t raw_full[2 * kMaxRaw], raw_empty[kMaxRaw], kv_full[4], kv_empty[8], s_full[2], p_full[2], o_done[2], spare;
+  uint64_t raw_full[2 * kMaxRaw], raw_empty[kMaxRaw], kv_full[kSlots], kv_empty[2 * kSlots], spare;
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];   // by softmax group and logit buffer
   uint32_t tmem;
   int abort;
-  int raw_bits[8];      // code width of the tile in a ring entry, 0 = a block id out of range
-  float rs[256];        // per row: log2(e) * scale * 2^exponent
+  int raw_bits[kMaxRaw];   // code width of the tile in a ring entry, 0 = a block id out of range
 };
-static_assert(sizeof(Misc) <= 2048, "misc area");
+template <int MODE>
+constexpr uint32_t smem_bytes() { return Geo<MODE>::kMiscAt + sizeof(Misc); }
+static_assert(smem_bytes<0>() <= 232448 && smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory");
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -115,19 +124,22 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 
-// Bounded wait; on running out the CTA gives up (abort), every other wait
-// runs out in turn.  No sleep between tries: every wait here is short and on
-// the critical path of the next role.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Misc* ms) {
-  for (unsigned i = 0; i < kTries; ++i)
-    if (phase_done(bar, parity)) return true;
+// Bounded wait.  When it runs out, abort is set and this and every later wait of
+// the block returns at once: the roles walk their loops to the end (every access
+// stays inside its buffers whatever they hold), the rows are written as 0 and
+// the error bit is raised.  No sleep between tries: every wait here is short and
+// on the critical path of the next role.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Misc* ms) {
+  if (phase_done(bar, parity)) return;
+  for (unsigned i = 1; i < kTries; ++i) {
+    if (phase_done(bar, parity)) return;
+    if ((i & 1023u) == 0 && *reinterpret_cast<volatile int*>(&ms->abort) != 0) return;
+  }
   *reinterpret_cast<volatile int*>(&ms->abort) = 1;
-  return false;
 }
-
-// The same by a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Misc* ms) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, ms));
+__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Misc* ms) {
+  wait(bar, parity, ms);
+  __syncwarp();
 }
 
 // A decoding lane's place: its first token in the tile and its 32-channel
@@ -308,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   griddep_wait();
   griddep_launch_dependents();
   const PoolView& P = a.pool;
-  Misc* ms = reinterpret_cast<Misc*>(sm + kMiscAt);
+  Misc* ms = reinterpret_cast<Misc*>(sm + G::kMiscAt);
+  float* row_scale = reinterpret_cast<float*>(sm + G::kQ);   // before the first decoded tile takes the place
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Item w = item_of<MODE>(a);
   const int hq = a.plan.n_q_heads, S = a.plan.n_splits, mb = a.plan.max_blocks_per_seq;
@@ -335,22 +348,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     return;
   }
 
-  // softmax warps with real rows, per row tile; MODE 0 drops its second tile
-  // when no row is in it
+  // Softmax warps with real rows, per group; MODE 0 drops its second row tile
+  // when no row is in it.  Steps of 64 columns of each group.
   const int warps0 = min(4, (w.rv - w.r0 + 31) / 32);
-  const int warps1 = MODE == 0 ? max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32)) : warps0;
-  const int lag = MODE == 0 && warps1 == 0 ? 1 : 2;       // logit buffers in use
-  const int units = w.n * (MODE == 0 ? lag : 1);          // (row tile, key tile) products
+  const int warps1 = MODE == 2 ? 0 : MODE == 1 ? warps0 : max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32));
+  const int groups = warps1 > 0 ? 2 : 1;
+  const int steps0 = (MODE == 1 ? (w.n + 1) / 2 : w.n) * G::STEPS, steps1 = (MODE == 1 ? w.n / 2 : w.n) * G::STEPS;
 
   if (tid == 0) {
     for (int i = 0; i < 2 * n_raw; ++i) mbar_init(&ms->raw_full[i], 1);
-    for (int i = 0; i < n_raw; ++i) mbar_init(&ms->raw_empty[i], kDecodeWarps / 2);
-    for (int i = 0; i < G::SLOTS; ++i) mbar_init(&ms->kv_full[i], kDecodeWarps / 2);
-    for (int i = 0; i < 2 * G::SLOTS; ++i) mbar_init(&ms->kv_empty[i], 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms->s_full[i], 1);
-      mbar_init(&ms->p_full[i], MODE != 0 ? warps0 : (i == 0 ? warps0 : max(1, warps1)));
-      mbar_init(&ms->o_done[i], 1);
+    for (int i = 0; i < n_raw; ++i) mbar_init(&ms->raw_empty[i], 4);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&ms->kv_full[i], 4);
+    for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&ms->kv_empty[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ms->s_full[i >> 1][i & 1], 1);
+      mbar_init(&ms->p_full[i >> 1][i & 1], i < 2 ? warps0 : max(1, warps1));
+      mbar_init(&ms->o_done[i >> 1][i & 1], 1);
     }
     mbar_init(&ms->spare, 1);
     ms->abort = 0;
@@ -389,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       // the row's largest magnitude comes to lie in [64, 128)
       const int e = m == 0.0f ? 0 : max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
       const float f = __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
-      if (j == 0) ms->rs[row] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e - 6) << 23);
+      if (j == 0) row_scale[row] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e - 6) << 23);
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -410,101 +423,101 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   const uint32_t tmem = ms->tmem;
   const int end = w.len + w.nn;                            // tokens of the sequence
   const int32_t* table = a.tables + static_cast<int64_t>(w.b) * mb;
+  const int group = warp >> 2;                             // of a softmax warp
+  const int local = (MODE == 0 && warp < 8 ? group * 128 : 0) + (warp & 3) * 32 + lane;
+  const float rs = row_scale[local];
+  __syncthreads();
 
-  if (warp == kFeedWarp) {
-    // ---- feed ------------------------------------------------------------------
-    int issued = 0, e = -1, f = -1;
-    uint32_t lap = 0;                                      // parity of n / n_raw
-    for (int n = 0; n < 2 * w.n; ++n) {
-      const int t = w.t0 + (n >> 1) * BN;
-      const int blk = __ldg(table + t / kBlockTokens);
-      if (++e == n_raw) e = 0, lap ^= 1;
-      if (++f == 2 * n_raw) f = 0;
-      if (!warp_wait(&ms->raw_empty[e], lap ^ 1, ms)) break;
-      uint64_t* full = &ms->raw_full[f];
-      uint8_t* dst = sm + kRawAt + e * raw_stride;
-      if (blk < 0 || blk >= P.n_blocks()) {
-        if (elect_one()) {
-          raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
-          ms->raw_bits[e] = 0;
-          mbar_arrive(full);
+  if (warp >= kMmaWarp) {
+    regs_down<kOtherRegs>();
+    if (warp == kFeedWarp) {
+      // ---- feed ----------------------------------------------------------------
+      if (elect_one()) {
+        int e = -1, f = -1;
+        uint32_t lap = 0;                                  // parity of n / n_raw
+        int n = 0;
+        for (; n < 2 * w.n; ++n) {
+          const int t = w.t0 + (n >> 1) * BN;
+          const int blk = __ldg(table + t / kBlockTokens);
+          if (++e == n_raw) e = 0, lap ^= 1;
+          if (++f == 2 * n_raw) f = 0;
+          wait(&ms->raw_empty[e], lap ^ 1, ms);
+          if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) break;
+          uint64_t* full = &ms->raw_full[f];
+          uint8_t* dst = sm + G::kRawAt + e * raw_stride;
+          if (blk < 0 || blk >= P.n_blocks()) {
+            raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
+            ms->raw_bits[e] = 0;
+            mbar_arrive(full);
+          } else {
+            const int bits = P.bits_of(blk);
+            const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
+            const int64_t row = (phys * P.n_kv_heads + w.h) * kBlockTokens + t % kBlockTokens;
+            const bool key = (n & 1) == 0;
+            const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
+                                             : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
+            const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
+                                              : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
+            const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
+            ms->raw_bits[e] = bits;
+            mbar_arrive_tx(full, cb + pb + 16);
+            bulk_g2s(dst, codes + row * (D / 8 * bits), cb, full);
+            if (pb > 0) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, full);
+            bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16, full);
+          }
         }
-      } else {
-        const int bits = P.bits_of(blk);
-        const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
-        const int64_t row = (phys * P.n_kv_heads + w.h) * kBlockTokens + t % kBlockTokens;
-        const bool key = (n & 1) == 0;
-        const uint8_t* codes = bits == 4 ? (key ? P.k_codes4 : P.v_codes4)
-                                         : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
-        const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
-                                          : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
-        const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
-        if (elect_one()) {
-          ms->raw_bits[e] = bits;
-          mbar_arrive_tx(full, cb + pb + 16);
-          bulk_g2s(dst, codes + row * (D / 8 * bits), cb, full);
-          if (pb > 0) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, full);
-          bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16, full);
-        }
+        if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)      // let the copies in flight land
+          for (int c = max(0, n - n_raw); c < n; ++c) mbar_wait(&ms->raw_full[c % (2 * n_raw)], (c / (2 * n_raw)) & 1);
       }
-      __syncwarp();
-      issued = n + 1;
-    }
-    if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)          // let the copies in flight land
-      for (int n = max(0, issued - n_raw); n < issued; ++n) mbar_wait(&ms->raw_full[n % (2 * n_raw)], (n / (2 * n_raw)) & 1);
-  } else if (warp == kMmaWarp) {
-    // ---- product ---------------------------------------------------------------
-    constexpr uint32_t kQk = mma_f16_desc(128, BN, false), kPv = mma_f16_desc(128, D, true);
-    const uint32_t q_at = smem_u32(sm), kv_at = q_at + G::kQ;
-    bool ok = true;
-    for (int u = 0; u < units + lag; ++u) {
-      if (u >= lag) {                                      // O += P V of unit v
-        const int v = u - lag, buf = v % lag;
-        const int j = MODE == 0 ? v / lag : v, n = 2 * j + 1, slot = n % G::SLOTS;
-        ok = warp_wait(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms) && warp_wait(&ms->p_full[buf], (v / lag) & 1, ms);
-        if (!ok) break;
-        tc_fence_after();
-        const int oi = MODE == 2 ? 0 : buf;
-        const uint64_t vd = smem_operand(kv_at + slot * G::kTile, BN * 128, 1024);
-        const uint32_t o = tmem + oi * 128, p = tmem + G::kSBase + buf * BN;
-        const bool first = MODE == 2 ? v == 0 : v < lag;
-        if (elect_one()) {
+    } else if (warp == kMmaWarp) {
+      // ---- product -------------------------------------------------------------
+      if (elect_one()) {
+        constexpr uint32_t kQk = mma_f16_desc(128, kCols, false), kPv = mma_f16_desc(128, D, true);
+        const uint64_t q0 = smem_operand(smem_u32(sm), 16, 1024), k0 = smem_operand(smem_u32(sm) + G::kQ, 16, 1024),
+                       v0 = smem_operand(smem_u32(sm) + G::kQ, BN * 128, 1024);
+        for (int u = 0; u < steps0 + 2; ++u) {
+          for (int s = 0; s < groups; ++s) {
+            const int steps = s == 0 ? steps0 : steps1;
+            const uint32_t logits = tmem + kSBase + s * (2 * kCols) + (u & 1) * kCols;   // of steps u - 2 and u
+            const int v = u - 2;
+            if (v >= 0 && v < steps) {                     // O += P V
+              const int j = MODE == 1 ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
+              wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
+              wait(&ms->p_full[s][v & 1], (v >> 1) & 1, ms);
+              tc_fence_after();
+              const uint64_t vd = v0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k) mma_ts(o, p + k * 8, vd + k * (2048 >> 4), kPv, !first || k > 0);
-          mma_commit(&ms->o_done[buf]);
-          if (MODE != 0 || buf == lag - 1) mma_commit(&ms->kv_empty[n % (2 * G::SLOTS)]);
-        }
-        __syncwarp();
-      }
-      if (u < units) {                                     // S = Q K^T of unit u
-        const int buf = u % lag;
-        const int j = MODE == 0 ? u / lag : u, n = 2 * j, slot = n % G::SLOTS;
-        ok = warp_wait(&ms->kv_full[slot], (n / G::SLOTS) & 1, ms);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t qd = smem_operand(q_at + (MODE == 0 ? buf * (128 * D * 2) : 0), 16, 1024);
-        const uint64_t kd = smem_operand(kv_at + slot * G::kTile, 16, 1024);
-        const uint32_t s = tmem + G::kSBase + buf * BN;
-        // (the product that read the weights in this buffer was issued
-        // before this one; products of one thread run in order)
-        if (elect_one()) {
+              for (int k = 0; k < kCols / 16; ++k) mma_ts(tmem + s * 128, logits + k * 8, vd + k * (2048 >> 4), kPv, v > 0 || k > 0);
+              mma_commit(&ms->o_done[s][v & 1]);
+              if (h == G::STEPS - 1 && (MODE != 0 || s == groups - 1)) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
+            }
+            if (u < steps) {                               // S = Q K^T
+              const int j = MODE == 1 ? 2 * (u / G::STEPS) + s : u / G::STEPS, h = u % G::STEPS, n = 2 * j;
+              wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
+              tc_fence_after();
+              const uint64_t qd = q0 + (MODE == 0 ? s * (128 * D * 2 >> 4) : 0);
+              const uint64_t kd = k0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
+              // (the product that read the weights in this buffer was issued
+              // before this one; products of one thread run in order)
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(s, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4),
-                   kQk, k > 0);
-          mma_commit(&ms->s_full[buf]);
-          if (MODE != 0 || buf == lag - 1) mma_commit(&ms->kv_empty[n % (2 * G::SLOTS)]);
+              for (int k = 0; k < D / 16; ++k)
+                mma_ss(logits, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                       kd + (((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4), kQk, k > 0);
+              mma_commit(&ms->s_full[s][u & 1]);
+              if (h == G::STEPS - 1 && (MODE != 0 || s == groups - 1)) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
+            }
+          }
         }
-        __syncwarp();
+        if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) {    // let the products in flight end
+          mma_commit(&ms->spare);
+          mbar_wait(&ms->spare, 0);
+        }
       }
     }
-    if (!ok) {
-      if (elect_one()) mma_commit(&ms->spare);
-      warp_wait(&ms->spare, 0, ms);
-    }
-  } else if (warp >= kDecodeWarp0 && warp < kMmaWarp) {
+    __syncwarp();
+  } else if (warp >= kDecodeWarp0) {
+    regs_down<kDecodeRegs>();
     // ---- decode ----------------------------------------------------------------
-    // four warps decode the keys, four the values
     const int dw = warp & 3, kind = (warp - kDecodeWarp0) >> 2;
     // a warp takes 8 tokens x 128 channels or 4 x 256 at a time, a lane 32
     // channels of one token; the tokens are skewed over the lanes so that both
@@ -517,17 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     int e = kind, f = kind;                                // n % n_raw, n % (2 n_raw)
     uint32_t lap = 0;                                      // parity of n / (2 n_raw)
     for (int n = kind; n < 2 * w.n; n += 2) {
-      const int slot = n % G::SLOTS;
-      if (!warp_wait(&ms->raw_full[f], lap, ms)) break;
+      warp_wait(&ms->raw_full[f], lap, ms);
       const int bits = ms->raw_bits[e];
-      const uint8_t* raw = sm + kRawAt + e * raw_stride;
+      const uint8_t* raw = sm + G::kRawAt + e * raw_stride;
       const uint8_t* params = raw + raw_stride - 16 - BN * (D / kGroup) * 4;
       const int t0 = w.t0 + (n >> 1) * BN;
       // which of the lane's four tokens count
       uint32_t live = 0;
       {
         const uint4 m = *reinterpret_cast<const uint4*>(raw + raw_stride - 16);
-        const uint32_t m0 = D == 128 || (t0 & 64) == 0 ? m.x : m.z, m1 = D == 128 || (t0 & 64) == 0 ? m.y : m.w;
+        const bool upper = D == 256 && (t0 & 64) != 0;
+        const uint32_t m0 = upper ? m.z : m.x, m1 = upper ? m.w : m.y;
         const uint32_t word[4] = {m0, D == 128 ? m1 : m0, D == 128 ? m.z : m1, D == 128 ? m.w : m1};
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -536,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         }
       }
       if (bits == 0) live = 0;
-      const int before = n - G::SLOTS;                     // the tile that was in the slot
-      if (before >= 0 && !warp_wait(&ms->kv_empty[before % (2 * G::SLOTS)], (before / (2 * G::SLOTS)) & 1, ms)) break;
-      uint8_t* dst = sm + G::kQ + slot * G::kTile + dst0;
+      const int before = n - kSlots;                       // the tile that was in the slot
+      if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
+      uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
       if (P.fp8) decode_tile<D, 0>(raw, params, ln, live, dst);
       else if (bits == 8) decode_tile<D, 8>(raw, params, ln, live, dst);
       else if (bits == 2) decode_tile<D, 2>(raw, params, ln, live, dst);
@@ -547,173 +560,159 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ms->raw_empty[e]);
-        mbar_arrive(&ms->kv_full[slot]);
+        mbar_arrive(&ms->kv_full[n % kSlots]);
       }
       if ((e += 2) >= n_raw) e -= n_raw;
       if ((f += 2) >= 2 * n_raw) f -= 2 * n_raw, lap ^= 1;
     }
-  } else if (warp < (MODE == 2 ? 4 : 8) && (warp & 3) < (warp < 4 ? warps0 : warps1)) {
-    // ---- softmax ---------------------------------------------------------------
-    const int st = MODE == 2 ? 0 : warp >> 2;              // stream
-    const int local = (MODE == 0 ? st * 128 : 0) + (warp & 3) * 32 + lane;
-    const int r = w.r0 + local;
-    const bool real = r < w.rv;
-    const int pos = w.len + min(r, w.rv - 1) / w.g;        // the row's position
-    const float rs = ms->rs[local];
-    const float sent = Q4KV_SENTINEL_LOGIT * kLog2e / rs;  // a remapped slot's logit before scaling
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t o_at = tmem + lanes + (MODE == 2 ? 0 : st * 128);
-    const int steps = MODE == 1 ? (w.n - st + 1) / 2 : w.n;
-    float m = -INFINITY, l = 0.0f;
-    bool poison = false, ok = true;
-    // Wait for the k-th product into the accumulator.  With two logit buffers
-    // on one accumulator the softmax can be a product further than in the
-    // other modes, so each buffer has its barrier.
-    auto product_done = [&](int k) {
-      return warp_wait(&ms->o_done[MODE == 2 ? k & 1 : st], (MODE == 2 ? k >> 1 : k) & 1, ms);
-    };
-
-    for (int k = 0; k < steps; ++k) {
-      const int buf = MODE == 2 ? k & 1 : st;
-      const uint32_t phase = (MODE == 2 ? k >> 1 : k) & 1;
-      const int t0 = w.t0 + (MODE == 1 ? 2 * k + st : k) * BN;
-      const uint32_t s_at = tmem + lanes + G::kSBase + buf * BN;
-      const int blk = __ldg(table + t0 / kBlockTokens);
-      const bool bad = blk < 0 || blk >= P.n_blocks();
-      const uint32_t* mw = P.mask + static_cast<int64_t>(blk) * kMaskWords + (t0 % kBlockTokens) / 32;
-      uint32_t any = 0;
-      if (!bad) {
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) any |= __ldg(mw + c);
+  } else {
+    regs_up<kSoftRegs>();
+    if ((warp & 3) < (group == 0 ? warps0 : warps1)) {
+      // ---- softmax -------------------------------------------------------------
+      const int r = w.r0 + local;
+      const bool real = r < w.rv;
+      const int pos = w.len + min(r, w.rv - 1) / w.g;      // the row's position
+      const float sent = Q4KV_SENTINEL_LOGIT * kLog2e / rs;   // a remapped slot's logit before scaling
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t o_at = tmem + lanes + group * 128;
+      const int steps = group == 0 ? steps0 : steps1;
+      // first token of step k
+      auto token = [&](int k) {
+        return w.t0 + (MODE == 1 ? (2 * (k / G::STEPS) + group) * BN + k % G::STEPS * kCols : k * kCols);
+      };
+      auto valid = [&](int blk) { return blk >= 0 && blk < P.n_blocks(); };
+      auto mask_at = [&](int blk, int t) {
+        return __ldg(reinterpret_cast<const uint2*>(P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 32));
+      };
+      // the block id and mask of the coming step are fetched a step ahead
+      float m = -INFINITY, l = 0.0f;
+      bool poison = false, bad = false;
+      uint2 gone = make_uint2(0u, 0u);
+      int blk1 = 0;
+      if (steps > 0) {
+        const int blk0 = __ldg(table + token(0) / kBlockTokens);
+        blk1 = steps > 1 ? __ldg(table + token(1) / kBlockTokens) : -1;
+        bad = !valid(blk0);
+        if (!bad) gone = mask_at(blk0, token(0));
       }
-      const int hi = pos - t0;                             // last column the row sees
-      const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
-      if (bad && hi >= 0 && lo < BN) poison = true;
-      const bool plain = __all_sync(0xffffffffu, hi >= BN - 1 && lo <= 0 && any == 0);
-      ok = warp_wait(&ms->s_full[buf], phase, ms);
-      if (!ok) break;
-      tc_fence_after();
-
-      if (!plain) {          // write the mask into the logits
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32(s_at + 32 * c, x);
-          tmem_wait_ld(x);
-          const int h1 = hi - 32 * c, l1 = lo - 32 * c;
-          uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
-          seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
-          const uint32_t away = bad ? 0u : __ldg(mw + c);
+      for (int k = 0; k < steps; ++k) {
+        const uint32_t s_at = tmem + lanes + kSBase + group * (2 * kCols) + (k & 1) * kCols;
+        const int t0 = token(k);
+        const bool bad1 = !valid(blk1);
+        uint2 gone1 = make_uint2(0u, 0u);
+        if (!bad1) gone1 = mask_at(blk1, token(k + 1));
+        blk1 = k + 2 < steps ? __ldg(table + token(k + 2) / kBlockTokens) : -1;
+        const int hi = pos - t0;                           // last column the row sees
+        const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
+        if (bad && hi >= 0 && lo < kCols) poison = true;
+        const bool plain = __all_sync(0xffffffffu, hi >= kCols - 1 && lo <= 0 && (gone.x | gone.y) == 0);
+        warp_wait(&ms->s_full[group][k & 1], (k >> 1) & 1, ms);
+        tc_fence_after();
+        uint32_t x[2][32];
+        tmem_ld32(s_at, x[0]);
+        tmem_ld32(s_at + 32, x[1]);
+        tmem_wait_ld(x[0]);
+        tmem_wait_ld(x[1]);
+        if (!plain) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = (away >> i) & 1u ? sent : __uint_as_float(x[i]);
-            x[i] = __float_as_uint((seen >> i) & 1u ? y : -INFINITY);
+          for (int c = 0; c < 2; ++c) {
+            const int h1 = hi - 32 * c, l1 = lo - 32 * c;
+            uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
+            seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
+            const uint32_t away = c == 0 ? gone.x : gone.y;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = (away >> i) & 1u ? sent : __uint_as_float(x[c][i]);
+              x[c][i] = __float_as_uint((seen >> i) & 1u ? y : -INFINITY);
+            }
           }
-          tmem_st32(s_at + 32 * c, x);
         }
-        tmem_wait_st();
-      }
-      // weights of 32 columns at a time
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      float off = kShift - (m == -INFINITY ? 0.0f : m);
-      const float2 rs2 = make_float2(rs, rs);
-#pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        uint32_t x[32];
-        tmem_ld32(s_at + 32 * c, x);
-        tmem_wait_ld(x);
-        float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+        float mx[4];
 #pragma unroll
-        for (int i = 2; i < 30; i += 4) {
-          mx[0] = max3(mx[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          mx[1] = max3(mx[1], __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-        }
-        const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))) * rs;
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(x[q & 1][q >> 1]), __uint_as_float(x[q & 1][(q >> 1) + 2]));
+#pragma unroll
+        for (int i = 4; i < 32; i += 4)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mx[q] = max3(mx[q], __uint_as_float(x[q & 1][i + (q >> 1)]), __uint_as_float(x[q & 1][i + 2 + (q >> 1)]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * rs;
         if (__any_sync(0xffffffffu, top > m + kLazy)) {
           // Move the reference: it stays a whole number, so everything scaled
           // by it scales by a power of two.
           const float to = ceilf(fmaxf(m, top));
           const float f = to == -INFINITY ? 1.0f : __int_as_float((static_cast<int>(fmaxf(m - to, -127.0f)) + 127) << 23);
           m = to;
-          off = kShift - (m == -INFINITY ? 0.0f : m);
-          if (k > 0 || c > 0) {
-            l *= f;
-            sum[0] = make_float2(sum[0].x * f, sum[0].y * f);
-            sum[1] = make_float2(sum[1].x * f, sum[1].y * f);
-            const __half2 f2 = __float2half2_rn(f);
+          l *= f;
+          if (k > 0) {
+            warp_wait(&ms->o_done[group][(k - 1) & 1], ((k - 1) >> 1) & 1, ms);
+            tc_fence_after();
 #pragma unroll 1
-            for (int e = 0; e < c; ++e) {                  // weights of this tile so far
-              uint32_t p[16];
-              tmem_ld16(s_at + 16 * e, p);
-              tmem_wait_ld(p);
+            for (int e = 0; e < D / 16; ++e) {
+              uint32_t o[16];
+              tmem_ld16(o_at + 16 * e, o);
+              tmem_wait_ld(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) p[i] = h2u(__hmul2(u2h(p[i]), f2));
-              tmem_st16(s_at + 16 * e, p);
-            }
-            if (k > 0) {
-              ok = product_done(k - 1);
-              tc_fence_after();
-#pragma unroll 1
-              for (int e = 0; ok && e < D / 16; ++e) {
-                uint32_t o[16];
-                tmem_ld16(o_at + 16 * e, o);
-                tmem_wait_ld(o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16(o_at + 16 * e, o);
-              }
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16(o_at + 16 * e, o);
             }
           }
         }
-        const float2 off2 = make_float2(off, off);
-        uint32_t p[16];
+        const float off = kShift - (m == -INFINITY ? 0.0f : m);
+        const float2 rs2 = make_float2(rs, rs), off2 = make_float2(off, off);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), rs2, off2);
-          // a quarter of the exponentials on the FMA pipe: the special-
-          // function unit (16 a clock) is what the tile waits for otherwise
-          const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
-          sum[i & 1] = __fadd2_rn(sum[i & 1], q);
-          p[i] = h2u(__floats2half2_rn(q.x, q.y));
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), rs2, off2);
+            // a quarter of the exponentials on the FMA pipe: the special-
+            // function unit (16 a clock) is what the tile waits for otherwise
+            const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], q);
+            p[i] = h2u(__floats2half2_rn(q.x, q.y));
+          }
+          tmem_st16(s_at + 16 * c, p);
         }
-        tmem_st16(s_at + 16 * c, p);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->p_full[group][k & 1]);
+        bad = bad1;
+        gone = gone1;
       }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (!ok) break;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->p_full[buf]);
-    }
 
-    // ---- result ----------------------------------------------------------------
-    if (ok && steps > 0) ok = product_done(steps - 1);
-    tc_fence_after();
-    const int i = r / w.g, head = w.h * w.g + r % w.g;
-    const int64_t row = (static_cast<int64_t>(w.b) * w.T + i) * hq + head;
-    const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? st : 0)) * all_rows + row;
-    const bool fine = ok && !poison && l > 0.0f;
-    if (partials > 1 && real) a.ws_ml[part] = make_float2(ok ? m : 0.0f, ok && !poison ? l : -1.0f);
-    if (ok && steps > 0) {
-      const float f = partials > 1 ? 1.0f : (fine ? 1.0f / l : 0.0f);
+      // ---- result --------------------------------------------------------------
+      if (steps > 0) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, ms);
+      const bool ok = __all_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ms->abort) == 0);
+      tc_fence_after();
+      const int i = r / w.g, head = w.h * w.g + r % w.g;
+      const int64_t row = (static_cast<int64_t>(w.b) * w.T + i) * hq + head;
+      const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? group : 0)) * all_rows + row;
+      const bool fine = ok && !poison && l > 0.0f;
+      if (partials > 1 && real) a.ws_ml[part] = make_float2(ok ? m : 0.0f, ok && !poison ? l : -1.0f);
+      if (steps > 0) {
+        const float f = partials > 1 ? 1.0f : (fine ? 1.0f / l : 0.0f);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        float y[32];
-        tmem_ld32(o_at + 32 * c, x);
-        tmem_wait_ld(x);
-        channel_order(x, f, y);
-        if (partials == 1 && !fine) {
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          float y[32];
+          tmem_ld32(o_at + 32 * c, x);
+          tmem_wait_ld(x);
+          channel_order(x, f, y);
+          if (partials == 1 && !fine) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0.0f;
-        }
-        if (real) {
-          if (partials > 1) store32(a.ws_o, Q4KV_F32, part * D + 32 * c, y);
-          else store32(a.out, a.out_dtype, w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + 32 * c, y);
+            for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+          }
+          if (real) {
+            if (partials > 1) store32(a.ws_o, Q4KV_F32, part * D + 32 * c, y);
+            else store32(a.out, a.out_dtype, w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + 32 * c, y);
+          }
         }
       }
+      tc_fence_before();
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (tid == 0 && ms->abort != 0) raise_error(P.error_word, Q4KV_DEVERR_TIMEOUT);
@@ -792,8 +791,13 @@ cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
   if (x > 0x7fffffff) return cudaErrorInvalidValue;
   const uint32_t codes = G::BN * G::D / 8 * (a.pool.n_q8 > 0 ? 8 : 4);
   const uint32_t stride = codes + G::BN * (G::D / kGroup) * 4 + 16;
-  const int n_raw = min(kMaxRaw, static_cast<int>(kRawRing / stride));
-  cudaError_t e = cudaFuncSetAttribute(extend_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const int n_raw = min(kMaxRaw, static_cast<int>(G::kRawRing / stride));
+  constexpr uint32_t kSmem = smem_bytes<MODE>();
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, extend_kernel<MODE>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs != kRegs) return cudaErrorInvalidKernelImage;   // the register shares would not add up
+  e = cudaFuncSetAttribute(extend_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(extend_kernel<MODE>, dim3(static_cast<unsigned>(x), p.n_kv_heads, p.batch), dim3(kThreads), kSmem, stream, a,
                  stride, n_raw);

@@ -1,11 +1,11 @@
 """Event model of the chunk-attention kernel's barriers (CPU).
 
-The kernel's roles (feed, key and value decoders, product, softmax) meet at
-mbarriers and wait by phase parity, which tells only two neighbouring phases of
-a barrier apart.  Here the roles run in random order, copies land in random
+The kernel's roles (feed, key and value decoders, product, softmax groups) meet
+at mbarriers and wait by phase parity, which tells only two neighbouring phases
+of a barrier apart.  Here the roles run in random order, copies land in random
 order and products finish in issue order; every use of a buffer checks that it
-holds what its user expects.  As controls, the layouts with one barrier per place
-(shared by keys and values) and with one barrier for two logit buffers fail."""
+holds what its user expects.  As controls, barriers shared by keys and values
+(with an odd number of places) and one barrier for both logit buffers fail."""
 import random
 
 import pytest
@@ -25,16 +25,23 @@ class Bar:
         return (self.done & 1) != parity
 
 
-def run(mode, lag, slots, n_raw, n, seed, shared=False, one_done=False):
+def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False):
+    """mode 0: groups with rows of their own; 1: groups on alternate tiles; 2: one step a tile."""
     r = random.Random(seed)
+    per = 1 if mode == 2 else 2                # softmax steps of a tile
     k_raw, k_slot = (n_raw, slots) if shared else (2 * n_raw, 2 * slots)
     raw_full, raw_empty = [Bar(1) for _ in range(k_raw)], [Bar(4) for _ in range(n_raw)]
     kv_full, kv_empty = [Bar(4) for _ in range(slots)], [Bar(1) for _ in range(k_slot)]
-    s_full, p_full, o_done = ([Bar(1) for _ in range(2)] for _ in range(3))
+    s_full, p_full, o_done = ([[Bar(1), Bar(1)] for _ in range(2)] for _ in range(3))
     raw, slot = [None] * n_raw, [(None, 0)] * slots
-    flying, queue, products = [], [], []
-    uses = {i: lag if mode == 0 else 1 for i in range(2 * n)}
-    units = n * (lag if mode == 0 else 1)
+    logits = [[None, None], [None, None]]      # what each buffer holds: ("S" or "P", step)
+    flying, queue = [], []
+    products = [set(), set()]
+    uses = {i: per * (groups if mode == 0 else 1) for i in range(2 * n)}
+    steps = [((n - s + 1) // 2 if mode == 1 else n) * per for s in range(groups)]
+
+    def tile(s, k):
+        return 2 * (k // per) + s if mode == 1 else k // per
 
     def feed():
         for i in range(2 * n):
@@ -64,54 +71,50 @@ def run(mode, lag, slots, n_raw, n, seed, shared=False, one_done=False):
             yield
 
     def product():
-        for u in range(units + lag):
-            if u >= lag:
-                v = u - lag
-                i = 2 * (v // lag if mode == 0 else v) + 1
-                while not kv_full[i % slots].ready((i // slots) & 1):
+        for u in range(steps[0] + 2):
+            for s in range(groups):
+                v = u - 2
+                if 0 <= v < steps[s]:
+                    i = 2 * tile(s, v) + 1
+                    while not kv_full[i % slots].ready((i // slots) & 1):
+                        yield
+                    assert slot[i % slots] == (i, 4), "values"
+                    while not p_full[s][v & 1].ready((v >> 1) & 1):
+                        yield
+                    assert logits[s][v & 1] == ("P", v), "weights"
+                    last = v % per == per - 1 and (mode != 0 or s == groups - 1)
+                    queue.append(("pv", s, v, i, last))
                     yield
-                assert slot[i % slots] == (i, 4), "values"
-                while not p_full[v % lag].ready((v // lag) & 1):
+                if u < steps[s]:
+                    i = 2 * tile(s, u)
+                    while not kv_full[i % slots].ready((i // slots) & 1):
+                        yield
+                    assert slot[i % slots] == (i, 4), "keys"
+                    last = u % per == per - 1 and (mode != 0 or s == groups - 1)
+                    queue.append(("qk", s, u, i, last))
                     yield
-                queue.append(("pv", v, i))
-                yield
-            if u < units:
-                i = 2 * (u // lag if mode == 0 else u)
-                while not kv_full[i % slots].ready((i // slots) & 1):
-                    yield
-                assert slot[i % slots] == (i, 4), "keys"
-                queue.append(("qk", u, i))
-                yield
 
-    def softmax(st):
-        steps = n if mode != 1 else (n - st + 1) // 2
-
-        def unit(k):
-            return k if mode == 2 else (lag * k + st if mode == 0 else 2 * k + st)
-
+    def softmax(s):
         def done(k):
-            if mode == 2 and not one_done:
-                return o_done[k & 1].ready((k >> 1) & 1)
-            return o_done[st].ready(k & 1)
+            return o_done[s][0].ready(k & 1) if one_done else o_done[s][k & 1].ready((k >> 1) & 1)
 
-        for k in range(steps):
-            buf, phase = (k & 1, k >> 1) if mode == 2 else (st, k)
-            while not s_full[buf].ready(phase & 1):
+        for k in range(steps[s]):
+            while not s_full[s][k & 1].ready((k >> 1) & 1):
                 yield
+            assert logits[s][k & 1] == ("S", k), "logits"
             if k and r.random() < 0.5:         # the maximum moves: the accumulator is rescaled
                 while not done(k - 1):
                     yield
-                assert unit(k - 1) in products, "accumulator not ready"
+                assert k - 1 in products[s], "accumulator not ready"
             yield
-            p_full[buf].arrive()
+            logits[s][k & 1] = ("P", k)
+            p_full[s][k & 1].arrive()
             yield
-        while steps and not done(steps - 1):
+        while steps[s] and not done(steps[s] - 1):
             yield
-        assert not steps or unit(steps - 1) in products, "result read too early"
+        assert not steps[s] or steps[s] - 1 in products[s], "result read too early"
 
-    roles = [feed(), product(), softmax(0)] + [decoder(k) for k in (0, 1) for _ in range(4)]
-    if mode == 1 or (mode == 0 and lag == 2):
-        roles.append(softmax(1))
+    roles = [feed(), product()] + [softmax(s) for s in range(groups)] + [decoder(k) for k in (0, 1) for _ in range(4)]
     idle = 0
     while roles:
         x = r.random()
@@ -122,15 +125,17 @@ def run(mode, lag, slots, n_raw, n, seed, shared=False, one_done=False):
             idle = 0
             continue
         if x < 0.3 and queue:
-            what, u, i = queue.pop(0)
+            what, s, u, i, last = queue.pop(0)
             assert slot[i % slots][0] == i, "operand overwritten"
             uses[i] -= 1
             if what == "qk":
-                s_full[u % lag].arrive()
+                logits[s][u & 1] = ("S", u)
+                s_full[s][u & 1].arrive()
             else:
-                products.append(u)
-                o_done[0 if mode == 2 and one_done else u % lag].arrive()
-            if mode != 0 or u % lag == lag - 1:
+                assert logits[s][u & 1] == ("P", u), "weights overwritten"
+                products[s].add(u)
+                o_done[s][0 if one_done else u & 1].arrive()
+            if last:
                 kv_empty[i % k_slot].arrive()
             idle = 0
             continue
@@ -143,25 +148,21 @@ def run(mode, lag, slots, n_raw, n, seed, shared=False, one_done=False):
         assert idle < 100000, "stuck"
 
 
-# mode, logit buffers, decoded tiles: two row tiles; two of them with one empty;
-# alternating key tiles; heads of 256
-SHAPES = [(0, 2, 3), (0, 1, 3), (1, 2, 4), (2, 2, 3)]
-
-
-@pytest.mark.parametrize("mode,lag,slots", SHAPES)
-@pytest.mark.parametrize("n_raw", [3, 7])
-def test_roles_never_meet_a_wrong_buffer(mode, lag, slots, n_raw):
+# two row tiles; one of them empty; alternate key tiles; heads of 256
+@pytest.mark.parametrize("mode,groups", [(0, 2), (0, 1), (1, 2), (2, 1)])
+@pytest.mark.parametrize("n_raw", [2, 3, 7])
+def test_roles_never_meet_a_wrong_buffer(mode, groups, n_raw):
     for n in (1, 2, 3, 5, 17):
         for seed in range(12):
-            run(mode, lag, slots, n_raw, n, seed)
+            run(mode, groups, n_raw, n, seed)
 
 
-@pytest.mark.parametrize("kw,shape", [({"shared": True}, (2, 2, 3)), ({"one_done": True}, (2, 2, 3))])
-def test_controls_fail(kw, shape):
-    failed = 0
-    for seed in range(60):
+@pytest.mark.parametrize("kw", [{"shared": True, "slots": 3}, {"shared": True, "n_raw": 3}, {"one_done": True}])
+def test_controls_fail(kw):
+    failed, n_raw = 0, kw.get("n_raw", 3)
+    for seed in range(80):
         try:
-            run(*shape, 3, 17, seed, **kw)
+            run(2, 1, n_raw, 17, seed, **{k: v for k, v in kw.items() if k != "n_raw"})
         except AssertionError:
             failed += 1
     assert failed > 0
