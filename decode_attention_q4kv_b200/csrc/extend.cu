@@ -86,30 +86,22 @@ struct Misc {
   uint32_t tmem;
   int abort;
   int raw_bits[kMaxRaw];   // code width of the tile in a ring entry, 0 = a block id out of range
+  // Remapped slots of key tile j and whether its block id is out of range, at
+  // j % 8, from the key decoders to the softmax.  (When tile j + 8 is decoded,
+  // the keys of tile j + 6 are used up, and the softmax is past tile j.)
+  alignas(16) uint32_t gone[8][4];
+  int bad[8];
+  int8_t exponent[256];    // per row: q was scaled by 2^(6 - exponent)
 };
 template <int MODE>
 constexpr uint32_t smem_bytes() { return Geo<MODE>::kMiscAt + sizeof(Misc); }
+static_assert(Geo<0>::kMiscAt % 16 == 0 && Geo<1>::kMiscAt % 16 == 0 && Geo<2>::kMiscAt % 16 == 0, "alignment");
 static_assert(smem_bytes<0>() <= 232448 && smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory");
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// 2^x = 2^n 2^f, n = rint(x), |f| <= 1/2, 2^f by the cubic of least relative
-// error on that interval (Remez exchange; 7.5e-5 = 2^-13.7, below the 2^-11 of
-// the weights' rounding to fp16).  x is held above -126, where the result no
-// longer counts.
-__device__ __forceinline__ float2 exp2_poly(float2 x) {
-  constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it leaves n in the low bits
-  x = make_float2(fmaxf(x.x, -126.0f), fmaxf(x.y, -126.0f));
-  const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
-  const float2 f = __fadd2_rn(x, __ffma2_rn(t, make_float2(-1.0f, -1.0f), make_float2(kMagic, kMagic)));
-  float2 p = __ffma2_rn(f, make_float2(0x1.c3f760p-5f, 0x1.c3f760p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
-  p = __ffma2_rn(p, f, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
-  p = __ffma2_rn(p, f, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 // One try of a wait, the hardware's own suspension only.
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
@@ -149,6 +141,12 @@ struct Lane {
   static constexpr __host__ __device__ int step(int d) { return d == 128 ? 32 : 16; }
 };
 
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 // 8 codes as 4 half pairs in the order above: fp16(code * s + z), one rounding.
 // 0x64xx is 1024 + xx in fp16: a mask and an or give codes exactly, less 1024.
 __device__ __forceinline__ void codes4(uint32_t w, __half2 s, __half2 z, uint32_t* o) {
@@ -156,8 +154,8 @@ __device__ __forceinline__ void codes4(uint32_t w, __half2 s, __half2 z, uint32_
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t v = w >> (8 * i);
-    const __half2 lo = __hsub2(u2h((v & 0x000F000Fu) | 0x64006400u), k1024);
-    const __half2 hi = __hfma2(u2h((v & 0x00F000F0u) | 0x64006400u), k16, k64);   // (1024 + 16 code) / 16 - 64
+    const __half2 lo = __hsub2(u2h(and_or(v, 0x000F000Fu, 0x64006400u)), k1024);
+    const __half2 hi = __hfma2(u2h(and_or(v, 0x00F000F0u, 0x64006400u)), k16, k64);   // (1024 + 16 code) / 16 - 64
     o[2 * i] = h2u(__hfma2(lo, s, z));
     o[2 * i + 1] = h2u(__hfma2(hi, s, z));
   }
@@ -166,14 +164,14 @@ __device__ __forceinline__ void codes8(uint32_t w0, uint32_t w1, __half2 s, __ha
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t v = __byte_perm(w0, w1, static_cast<uint32_t>(i | i << 4 | (4 + i) << 8 | (4 + i) << 12));
-    o[i] = h2u(__hfma2(__hsub2(u2h((v & 0x00FF00FFu) | 0x64006400u), __float2half2_rn(1024.0f)), s, z));
+    o[i] = h2u(__hfma2(__hsub2(u2h(and_or(v, 0x00FF00FFu, 0x64006400u)), __float2half2_rn(1024.0f)), s, z));
   }
 }
 __device__ __forceinline__ void codes2(uint32_t w16, __half2 s, __half2 z, uint32_t* o) {   // codes 0-3, codes 4-7 in halves
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float f = 1.0f / static_cast<float>(1 << (2 * i));
-    const __half2 h = __hfma2(u2h((w16 & (0x00030003u << (2 * i))) | 0x64006400u), __float2half2_rn(f),
+    const __half2 h = __hfma2(u2h(and_or(w16, 0x00030003u << (2 * i), 0x64006400u)), __float2half2_rn(f),
                               __float2half2_rn(-1024.0f * f));
     o[i] = h2u(__hfma2(h, s, z));
   }
@@ -250,26 +248,10 @@ __device__ __forceinline__ void channel_order(const uint32_t (&r)[32], float f, 
       y[8 * k + 4 + i] = __uint_as_float(r[8 * k + 2 * i + 1]) * f;
     }
 }
-__device__ __forceinline__ void store32(void* out, int dtype, int64_t at, const float (&y)[32]) {
-  if (dtype == Q4KV_F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    return;
-  }
-  uint32_t w[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (dtype == Q4KV_F16) {
-      w[i] = h2u(__floats2half2_rn(y[2 * i], y[2 * i + 1]));
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  uint4* o = reinterpret_cast<uint4*>(static_cast<__half*>(out) + at);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+__device__ __forceinline__ uint32_t pack16(int dtype, float x, float y) {
+  if (dtype == Q4KV_F16) return h2u(__floats2half2_rn(x, y));
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The part of the work one CTA has; every thread computes the same.
@@ -321,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   griddep_launch_dependents();
   const PoolView& P = a.pool;
   Misc* ms = reinterpret_cast<Misc*>(sm + G::kMiscAt);
-  float* row_scale = reinterpret_cast<float*>(sm + G::kQ);   // before the first decoded tile takes the place
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Item w = item_of<MODE>(a);
   const int hq = a.plan.n_q_heads, S = a.plan.n_splits, mb = a.plan.max_blocks_per_seq;
@@ -331,11 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   if (w.bad && w.nn > 0 && tid == 0) raise_error(P.error_word, Q4KV_DEVERR_SEQ_LEN);
   if (partials == 1) {   // rows of no real token are 0 (the merge sees to them otherwise)
     const int z0 = w.bad ? w.r0 : max(w.r0, w.rv);
-    for (int x = tid; x < (w.r1 - z0) * (D / 32); x += kThreads) {
-      const int r = z0 + x / (D / 32);
-      const float zero[32] = {};
-      store32(a.out, a.out_dtype, w.b * a.o_seq_stride + (r / w.g) * a.o_token_stride +
-              static_cast<int64_t>(w.h * w.g + r % w.g) * D + (x % (D / 32)) * 32, zero);
+    const int size = a.out_dtype == Q4KV_F32 ? 4 : 2, pieces = D * size / 16;
+    for (int x = tid; x < (w.r1 - z0) * pieces; x += kThreads) {
+      const int r = z0 + x / pieces;
+      uint8_t* row = static_cast<uint8_t*>(a.out) + (w.b * a.o_seq_stride + (r / w.g) * a.o_token_stride +
+                                                     static_cast<int64_t>(w.h * w.g + r % w.g) * D) * size;
+      reinterpret_cast<uint4*>(row)[x % pieces] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (w.bad || w.rv <= w.r0) return;
@@ -371,24 +353,41 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   }
   if (warp == kMmaWarp) tmem_alloc(&ms->tmem, 512);
 
-  // Q: rotate, scale each row by a power of two, round to fp16
-  {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  const int end = w.len + w.nn;                            // tokens of the sequence
+  const int32_t* table = a.tables + static_cast<int64_t>(w.b) * mb;
+  const int group = warp >> 2;                             // of a softmax warp
+
+  if (warp < kMmaWarp) {
+    // Q: rotate, scale each row by a power of two, round to fp16.  Rows of no
+    // real token are left as they are: no other row depends on them.
     using Sh = Shape<D>;
-    const int r = lane / Sh::LPV, j = lane % Sh::LPV;
-    for (int p = warp; p < G::R / Sh::VPW; p += kThreads / 32) {
-      const int row = p * Sh::VPW + r, rr = w.r0 + row;
-      float2 x[8];
+    constexpr int kPasses = G::R / Sh::VPW / 16;           // of a warp
+    const int rl = lane / Sh::LPV, j = lane % Sh::LPV;
+    uint4 in[kPasses][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = make_float2(0.0f, 0.0f);
+    for (int p = 0; p < kPasses; ++p) {
+      const int rr = w.r0 + (p * 16 + warp) * Sh::VPW + rl;
+      in[p][0] = in[p][1] = make_uint4(0u, 0u, 0u, 0u);
       if (rr < w.rv) {
-        const int64_t at = w.b * a.q_seq_stride + (rr / w.g) * a.q_token_stride +
-                           static_cast<int64_t>(w.h * w.g + rr % w.g) * D + j * kEPL;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at);
-        const uint4 w0 = __ldg(src), w1 = __ldg(src + 1);
-        if (a.q_dtype == Q4KV_F16) unpack16<__half>(w0, w1, x);
-        else unpack16<__nv_bfloat16>(w0, w1, x);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __half*>(a.q) + w.b * a.q_seq_stride + (rr / w.g) * a.q_token_stride +
+            static_cast<int64_t>(w.h * w.g + rr % w.g) * D + j * kEPL);
+        in[p][0] = __ldg(src);
+        in[p][1] = __ldg(src + 1);
       }
-      __syncwarp();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int row = (p * 16 + warp) * Sh::VPW + rl;
+      if (w.r0 + (p * 16 + warp) * Sh::VPW >= w.rv) break; // (the whole warp)
+      float2 x[8];
+      if (a.q_dtype == Q4KV_F16) unpack16<__half>(in[p][0], in[p][1], x);
+      else unpack16<__nv_bfloat16>(in[p][0], in[p][1], x);
       if (P.k_rotated) {
         rotate_pairs<D>(x, j);
 #pragma unroll
@@ -400,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
       for (int st = 1; st < Sh::LPV; st <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, st));
       // the row's largest magnitude comes to lie in [64, 128)
-      const int e = m == 0.0f ? 0 : max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100);
+      const int e = m == 0.0f ? 0 : min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100), 127);
       const float f = __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
-      if (j == 0) row_scale[row] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + e - 6) << 23);
+      if (j == 0) ms->exponent[row] = static_cast<int8_t>(e);
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -415,19 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       *reinterpret_cast<uint4*>(base + ((c ^ (lr & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4*>(base + (((c + 1) ^ (lr & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    fence_async_shared();
   }
-  fence_async_shared();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = ms->tmem;
-  const int end = w.len + w.nn;                            // tokens of the sequence
-  const int32_t* table = a.tables + static_cast<int64_t>(w.b) * mb;
-  const int group = warp >> 2;                             // of a softmax warp
-  const int local = (MODE == 0 && warp < 8 ? group * 128 : 0) + (warp & 3) * 32 + lane;
-  const float rs = row_scale[local];
-  __syncthreads();
+  // everyone but the feed, which has no use for Q, waits for it
+  if (warp != kFeedWarp) asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
 
+  struct {
+    float m, l;
+    bool poison, any;
+  } result = {-INFINITY, 0.0f, false, false};
   if (warp >= kMmaWarp) {
     regs_down<kOtherRegs>();
     if (warp == kFeedWarp) {
@@ -549,6 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         }
       }
       if (bits == 0) live = 0;
+      if (kind == 0 && dw == 0 && lane < 4) {
+        const int j = (n >> 1) & 7;
+        const uint32_t* mask = reinterpret_cast<const uint32_t*>(raw + raw_stride - 16);
+        ms->gone[j][lane] = bits == 0 ? 0u : mask[D == 256 && (t0 & 64) != 0 ? (lane & 1) + 2 : lane];
+        if (lane == 0) ms->bad[j] = bits == 0;
+      }
       const int before = n - kSlots;                       // the tile that was in the slot
       if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
@@ -569,9 +570,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     regs_up<kSoftRegs>();
     if ((warp & 3) < (group == 0 ? warps0 : warps1)) {
       // ---- softmax -------------------------------------------------------------
+      const int local = (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
       const int r = w.r0 + local;
       const bool real = r < w.rv;
       const int pos = w.len + min(r, w.rv - 1) / w.g;      // the row's position
+      // log2(e) * scale * 2^exponent: from products to logits (rows behind the
+      // last real one take its place)
+      const float rs = a.scale * kLog2e *
+                       __uint_as_float(static_cast<uint32_t>(127 - 6 + ms->exponent[min(r, w.rv - 1) - w.r0]) << 23);
+      // positions of the warp's first and last row: a step that all of them see
+      // whole needs no mask
+      const int pos_first = w.len + (w.r0 + local - lane) / w.g, pos_last = w.len + min(w.r0 + local - lane + 31, w.rv - 1) / w.g;
       const float sent = Q4KV_SENTINEL_LOGIT * kLog2e / rs;   // a remapped slot's logit before scaling
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t o_at = tmem + lanes + group * 128;
@@ -580,39 +589,27 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       auto token = [&](int k) {
         return w.t0 + (MODE == 1 ? (2 * (k / G::STEPS) + group) * BN + k % G::STEPS * kCols : k * kCols);
       };
-      auto valid = [&](int blk) { return blk >= 0 && blk < P.n_blocks(); };
-      auto mask_at = [&](int blk, int t) {
-        return __ldg(reinterpret_cast<const uint2*>(P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 32));
-      };
-      // the block id and mask of the coming step are fetched a step ahead
       float m = -INFINITY, l = 0.0f;
-      bool poison = false, bad = false;
-      uint2 gone = make_uint2(0u, 0u);
-      int blk1 = 0;
-      if (steps > 0) {
-        const int blk0 = __ldg(table + token(0) / kBlockTokens);
-        blk1 = steps > 1 ? __ldg(table + token(1) / kBlockTokens) : -1;
-        bad = !valid(blk0);
-        if (!bad) gone = mask_at(blk0, token(0));
-      }
+      bool poison = false;
       for (int k = 0; k < steps; ++k) {
         const uint32_t s_at = tmem + lanes + kSBase + group * (2 * kCols) + (k & 1) * kCols;
         const int t0 = token(k);
-        const bool bad1 = !valid(blk1);
-        uint2 gone1 = make_uint2(0u, 0u);
-        if (!bad1) gone1 = mask_at(blk1, token(k + 1));
-        blk1 = k + 2 < steps ? __ldg(table + token(k + 2) / kBlockTokens) : -1;
         const int hi = pos - t0;                           // last column the row sees
         const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
-        if (bad && hi >= 0 && lo < kCols) poison = true;
-        const bool plain = __all_sync(0xffffffffu, hi >= kCols - 1 && lo <= 0 && (gone.x | gone.y) == 0);
         warp_wait(&ms->s_full[group][k & 1], (k >> 1) & 1, ms);
         tc_fence_after();
         uint32_t x[2][32];
         tmem_ld32(s_at, x[0]);
         tmem_ld32(s_at + 32, x[1]);
+        // (the key decoders wrote this before the tile that the logits come from)
+        const int j = MODE == 1 ? 2 * (k / G::STEPS) + group : k / G::STEPS;
+        const uint2 gone = *reinterpret_cast<const uint2*>(&ms->gone[j & 7][2 * (k % G::STEPS)]);
+        const bool bad = ms->bad[j & 7] != 0;
+        const bool plain = pos_first - t0 >= kCols - 1 && (a.plan.window == 0 || pos_last - a.plan.window < t0) &&
+                           (gone.x | gone.y) == 0 && !bad;
         tmem_wait_ld(x[0]);
         tmem_wait_ld(x[1]);
+        if (bad && hi >= 0 && lo < kCols) poison = true;
         if (!plain) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -636,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
           for (int q = 0; q < 4; ++q)
             mx[q] = max3(mx[q], __uint_as_float(x[q & 1][i + (q >> 1)]), __uint_as_float(x[q & 1][i + 2 + (q >> 1)]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * rs;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+        if (__any_sync(0xffffffffu, real && top > m + kLazy)) {
           // Move the reference: it stays a whole number, so everything scaled
           // by it scales by a power of two.
           const float to = ceilf(fmaxf(m, top));
@@ -666,9 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), rs2, off2);
-            // a quarter of the exponentials on the FMA pipe: the special-
-            // function unit (16 a clock) is what the tile waits for otherwise
-            const float2 q = i % 4 == 3 ? exp2_poly(e) : make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum[i & 1] = __fadd2_rn(sum[i & 1], q);
             p[i] = h2u(__floats2half2_rn(q.x, q.y));
           }
@@ -679,40 +674,77 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->p_full[group][k & 1]);
-        bad = bad1;
-        gone = gone1;
       }
 
-      // ---- result --------------------------------------------------------------
       if (steps > 0) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, ms);
-      const bool ok = __all_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&ms->abort) == 0);
-      tc_fence_after();
-      const int i = r / w.g, head = w.h * w.g + r % w.g;
-      const int64_t row = (static_cast<int64_t>(w.b) * w.T + i) * hq + head;
-      const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? group : 0)) * all_rows + row;
-      const bool fine = ok && !poison && l > 0.0f;
-      if (partials > 1 && real) a.ws_ml[part] = make_float2(ok ? m : 0.0f, ok && !poison ? l : -1.0f);
-      if (steps > 0) {
-        const float f = partials > 1 ? 1.0f : (fine ? 1.0f / l : 0.0f);
+      result.m = m;
+      result.l = l;
+      result.poison = poison;
+      result.any = steps > 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();         // every product is done: the tiles' place is free
+  tc_fence_after();
+
+  if (warp < 8 && (warp & 3) < (group == 0 ? warps0 : warps1)) {
+    // ---- result ----------------------------------------------------------------
+    // A warp's 32 rows go through shared memory, 16 bytes a lane and swizzled by
+    // the row, so that every store to global memory is of whole rows.
+    const bool ok = ms->abort == 0;
+    const int first = w.r0 + (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32, r = first + lane;
+    const bool fine = ok && !result.poison && result.l > 0.0f;
+    const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? group : 0)) * all_rows;
+    auto row_of = [&](int q) {                             // (sequence, token, head) of tile row q
+      return (static_cast<int64_t>(w.b) * w.T + q / w.g) * hq + w.h * w.g + q % w.g;
+    };
+    if (partials > 1 && r < w.rv) a.ws_ml[part + row_of(r)] = make_float2(ok ? result.m : 0.0f, ok && !result.poison ? result.l : -1.0f);
+    if (result.any) {
+      const bool wide = partials > 1 || a.out_dtype == Q4KV_F32;
+      const int pieces = wide ? D / 4 : D / 8;             // 16-byte pieces of a row
+      uint8_t* stage = sm + G::kQ + warp * (32 * D * 4);
+      const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 128;
+      const float f = partials > 1 ? 1.0f : (fine ? 1.0f / result.l : 0.0f);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          float y[32];
-          tmem_ld32(o_at + 32 * c, x);
-          tmem_wait_ld(x);
-          channel_order(x, f, y);
-          if (partials == 1 && !fine) {
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        float y[32];
+        tmem_ld32(o_at + 32 * c, x);
+        tmem_wait_ld(x);
+        channel_order(x, f, y);
+        if (partials == 1 && !fine) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = 0.0f;
-          }
-          if (real) {
-            if (partials > 1) store32(a.ws_o, Q4KV_F32, part * D + 32 * c, y);
-            else store32(a.out, a.out_dtype, w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + 32 * c, y);
-          }
+          for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+        }
+        uint8_t* mine = stage + lane * (pieces * 16);
+        if (wide) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(mine + ((8 * c + e) ^ (lane & 7)) * 16) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(mine + ((4 * c + e) ^ (lane & 7)) * 16) =
+                make_uint4(pack16(a.out_dtype, y[8 * e], y[8 * e + 1]), pack16(a.out_dtype, y[8 * e + 2], y[8 * e + 3]),
+                           pack16(a.out_dtype, y[8 * e + 4], y[8 * e + 5]), pack16(a.out_dtype, y[8 * e + 6], y[8 * e + 7]));
         }
       }
-      tc_fence_before();
+      __syncwarp();
+      const int rows = min(32, w.rv - first);
+      for (int x = lane; x < rows * pieces; x += 32) {
+        const int q = x / pieces, e = x % pieces;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + q * (pieces * 16) + (e ^ (q & 7)) * 16);
+        const int rq = first + q;
+        if (partials > 1) {
+          *reinterpret_cast<uint4*>(a.ws_o + (part + row_of(rq)) * D + e * 4) = v;
+        } else {
+          const int64_t at = w.b * a.o_seq_stride + (rq / w.g) * a.o_token_stride + static_cast<int64_t>(w.h * w.g + rq % w.g) * D;
+          if (wide) *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at + e * 4) = v;
+          else *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at + e * 8) = v;
+        }
+      }
     }
+    tc_fence_before();
   }
   __syncthreads();
   if (tid == 0 && ms->abort != 0) raise_error(P.error_word, Q4KV_DEVERR_TIMEOUT);
