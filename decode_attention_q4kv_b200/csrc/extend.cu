@@ -6,21 +6,20 @@
 // their keys in tiles, S = Q K^T and O += P V on the tensor cores (fp16
 // operands, fp32 accumulators in tensor memory).
 //
-// Warp roles (20 warps, the last two idle):
-//   softmax  two groups of four warps, one row per thread: maximum, weights, sum
-//            of 64 columns at a time.  The weights go back into the tensor memory
-//            that held the logits, and are the A operand of the second product.
+// Warp roles (28 warps, the last two idle):
+//   softmax  four groups of four warps, one row per thread: maximum, weights, sum
+//            of 64 columns at a time (a step).  Two groups share the rows of one
+//            accumulator and take its steps by turns, each with a logit buffer of
+//            its own: while the weights of one step are made, the logits of the
+//            next are loaded, and the products around them run.  The weights go
+//            back into the tensor memory that held the logits, and are the A
+//            operand of the second product.
 //   decode   four warps turn the keys' codes into fp16, four the values', in the
 //            layout the tensor cores read (rows of 128 bytes, 128-byte swizzle);
 //            remapped slots and slots past the end become zeros
 //   product  one thread issues the matrix products
 //   feed     one thread copies each tile's packed codes, scales and mask into a
 //            ring in shared memory (bulk copies)
-// A softmax group has two buffers of 64 logit columns: while it works on one, the
-// product of the weights before and the logits after run.  (With one buffer of
-// 128 columns the group waited for both products and every hand-over in turn;
-// leaving out the products and the exponentials then saved only 40 % of the
-// time.)
 //
 // Within 8 channels the decoded order is 0 4 1 5 2 6 3 7 (what one mask and one
 // subtraction per pair of codes leave); q is stored in the same order and the
@@ -41,11 +40,12 @@
 namespace q4kv {
 namespace {
 
-constexpr int kDecodeWarp0 = 8, kMmaWarp = 16, kFeedWarp = 17;
-constexpr int kThreads = 20 * 32;
-// Registers: 96 a thread at launch, shared out anew by role.
-constexpr int kRegs = 96, kSoftRegs = 120, kDecodeRegs = 80, kOtherRegs = 80;
-static_assert(8 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 20 * kRegs, "register shares");
+constexpr int kDecodeWarp0 = 16, kMmaWarp = 24, kFeedWarp = 25;
+constexpr int kThreads = 28 * 32;
+// Registers: 72 a thread at launch, shared out anew by role.
+constexpr int kRegs = 72, kSoftRegs = 88, kDecodeRegs = 48, kOtherRegs = 56;
+static_assert(16 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 28 * kRegs, "register shares");
+constexpr float kNone = -1.0e30f; // reference maximum of a row that has seen nothing
 constexpr int kCols = 64;        // logit columns of a softmax step
 constexpr int kSlots = 4;        // decoded tiles
 constexpr uint32_t kTile = 32768;// bytes of a decoded tile
@@ -56,10 +56,10 @@ constexpr float kLazy = 8.0f;    // growth of the maximum (log2) that moves it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 
-// MODE 0: D = 128, two row tiles of 128, a softmax group each.
-// MODE 1: D = 128, one row tile; the two softmax groups take alternate key tiles
-//         with their own accumulators (two partial results).
-// MODE 2: D = 256, one row tile, one softmax group.
+// MODE 0: D = 128, two row tiles of 128, two softmax groups each.
+// MODE 1: D = 128, one row tile; the two pairs of softmax groups take alternate
+//         key tiles with their own accumulators (two partial results).
+// MODE 2: D = 256, one row tile, two softmax groups.
 template <int MODE>
 struct Geo {
   static constexpr int D = MODE == 2 ? 256 : 128;
@@ -70,7 +70,7 @@ struct Geo {
   static constexpr int R = 128 * QT;
   static constexpr uint32_t kQ = QT * 128 * D * 2;
   static constexpr uint32_t kRawAt = kQ + kSlots * kTile;
-  static constexpr uint32_t kRawRing = MODE == 1 ? 67616 : 34848;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
+  static constexpr uint32_t kRawRing = MODE == 1 ? 65600 : 32800;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
   static constexpr uint32_t kMiscAt = kRawAt + kRawRing;
 };
 
@@ -82,15 +82,18 @@ struct Misc {
   // wait on a barrier only after it has seen the phase before; on a barrier
   // shared by both kinds the phase before would be the other warps' business.
   uint64_t raw_full[2 * kMaxRaw], raw_empty[kMaxRaw], kv_full[kSlots], kv_empty[2 * kSlots], spare;
-  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];   // by softmax group and logit buffer
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];   // by accumulator and logit buffer
+  uint64_t turn[2][4];     // by accumulator and quarter of its rows: the reference after a step is known
   uint32_t tmem;
   int abort;
   int raw_bits[kMaxRaw];   // code width of the tile in a ring entry, 0 = a block id out of range
+  int raw_block[kMaxRaw];  // and the index of its block among those of its width
   // Remapped slots of key tile j and whether its block id is out of range, at
   // j % 8, from the key decoders to the softmax.  (When tile j + 8 is decoded,
   // the keys of tile j + 6 are used up, and the softmax is past tile j.)
   alignas(16) uint32_t gone[8][4];
   int bad[8];
+  float reference[256];    // per row: the reference maximum after the last step that settled
   int8_t exponent[256];    // per row: q was scaled by 2^(6 - exponent)
 };
 template <int MODE>
@@ -196,44 +199,37 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
   constexpr int ROW = D / 8 * W;                       // bytes of a token
   const uint8_t* src = raw + ln.t * ROW + ln.u * 4 * W;
 #pragma unroll 1
-  for (int i2 = 0; i2 < 4; i2 += 2) {
-    uint32_t w[2][W], sz[2] = {0u, 0u};
+  for (int it = 0; it < 4; ++it) {
+    const uint8_t* p = src + it * TS * ROW;
+    uint32_t w[W], sz = 0;
+    if (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* p = src + (i2 + i) * TS * ROW;
-      if (W == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[i][0] = x.x;
-        w[i][1] = x.y;
-      } else {
-#pragma unroll
-        for (int q = 0; q < W / 4; ++q) {
-          const uint4 x = reinterpret_cast<const uint4*>(p)[q];
-          w[i][4 * q] = x.x;
-          w[i][4 * q + 1] = x.y;
-          w[i][(4 * q + 2) % W] = x.z;
-          w[i][(4 * q + 3) % W] = x.w;
-        }
+      for (int q = 0; q < W / 4; ++q) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[q];
+        w[4 * q] = x.x;
+        w[4 * q + 1] = x.y;
+        w[(4 * q + 2) % W] = x.z;
+        w[(4 * q + 3) % W] = x.w;
       }
-      if (BITS != 0)
-        sz[i] = *reinterpret_cast<const uint32_t*>(params + ((ln.t + (i2 + i) * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
     }
+    if (BITS != 0) sz = *reinterpret_cast<const uint32_t*>(params + ((ln.t + it * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
+    const bool on = (live >> it) & 1u;
+    const __half2 q = u2h(on ? sz : 0u);
+    const __half2 s = __low2half2(q), z = __high2half2(q);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool on = (live >> (i2 + i)) & 1u;
-      const __half2 q = u2h(on ? sz[i] : 0u);
-      const __half2 s = __low2half2(q), z = __high2half2(q);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[4];
-        if (BITS == 0) codes_fp8(w[i][(2 * c) % W], w[i][(2 * c + 1) % W], on, o);
-        else if (BITS == 8) codes8(w[i][(2 * c) % W], w[i][(2 * c + 1) % W], s, z, o);
-        else if (BITS == 4) codes4(w[i][c % W], s, z, o);
-        else codes2(__byte_perm(w[i][(c >> 1) % W], 0, c & 1 ? 0x4342 : 0x4140), s, z, o);
-        // (the lane's tokens are the same modulo 8)
-        *reinterpret_cast<uint4*>(dst + (i2 + i) * (TS / 8) * 1024 + (((4 * (ln.u & 1) + c) ^ (ln.t & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      }
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[4];
+      if (BITS == 0) codes_fp8(w[(2 * c) % W], w[(2 * c + 1) % W], on, o);
+      else if (BITS == 8) codes8(w[(2 * c) % W], w[(2 * c + 1) % W], s, z, o);
+      else if (BITS == 4) codes4(w[c % W], s, z, o);
+      else codes2(__byte_perm(w[(c >> 1) % W], 0, c & 1 ? 0x4342 : 0x4140), s, z, o);
+      // (the lane's tokens are the same modulo 8)
+      *reinterpret_cast<uint4*>(dst + it * (TS / 8) * 1024 + (((4 * (ln.u & 1) + c) ^ (ln.t & 7)) << 4)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -330,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     return;
   }
 
-  // Softmax warps with real rows, per group; MODE 0 drops its second row tile
-  // when no row is in it.  Steps of 64 columns of each group.
+  // Softmax warps (of a group) with real rows, per accumulator; MODE 0 drops its second row tile
+  // when no row is in it.  Steps of 64 columns of each accumulator.
   const int warps0 = min(4, (w.rv - w.r0 + 31) / 32);
   const int warps1 = MODE == 2 ? 0 : MODE == 1 ? warps0 : max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32));
   const int groups = warps1 > 0 ? 2 : 1;
@@ -348,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       mbar_init(&ms->o_done[i >> 1][i & 1], 1);
     }
     mbar_init(&ms->spare, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&ms->turn[i >> 2][i & 3], 1);
     ms->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -359,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   const uint32_t tmem = ms->tmem;
   const int end = w.len + w.nn;                            // tokens of the sequence
   const int32_t* table = a.tables + static_cast<int64_t>(w.b) * mb;
-  const int group = warp >> 2;                             // of a softmax warp
+  // of a softmax warp: its accumulator and its parity of steps
+  const int group = MODE == 2 ? warp >> 3 : (warp >> 3) & 1, side = (warp >> 2) & 1;
 
-  if (warp < kMmaWarp) {
+  if (warp < kDecodeWarp0) {
     // Q: rotate, scale each row by a power of two, round to fp16.  Rows of no
     // real token are left as they are: no other row depends on them.
     using Sh = Shape<D>;
@@ -416,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     fence_async_shared();
   }
-  // everyone but the feed, which has no use for Q, waits for it
-  if (warp != kFeedWarp) asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
+  // those that use Q wait for it
+  if (warp <= kMmaWarp && (warp < kDecodeWarp0 || warp == kMmaWarp)) asm volatile("bar.sync 1, %0;" ::"n"(17 * 32) : "memory");
 
   struct {
     float m, l;
     bool poison, any;
-  } result = {-INFINITY, 0.0f, false, false};
+  } result = {kNone, 0.0f, false, false};
   if (warp >= kMmaWarp) {
     regs_down<kOtherRegs>();
     if (warp == kFeedWarp) {
@@ -453,8 +451,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                                              : (bits == 8 ? (key ? P.k_codes8 : P.v_codes8) : (key ? P.k_codes2 : P.v_codes2));
             const __half2* params = bits == 4 ? (key ? P.k_params4 : P.v_params4)
                                               : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
-            const uint32_t cb = BN * D / 8 * bits, pb = P.fp8 ? 0 : BN * (D / kGroup) * 4;
+            // (the scales of 8-bit codes stay in global memory: the ring has no room for them)
+            const uint32_t cb = BN * D / 8 * bits, pb = bits == 8 ? 0 : BN * (D / kGroup) * 4;
             ms->raw_bits[e] = bits;
+            ms->raw_block[e] = static_cast<int>(phys);
             mbar_arrive_tx(full, cb + pb + 16);
             bulk_g2s(dst, codes + row * (D / 8 * bits), cb, full);
             if (pb > 0) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, full);
@@ -554,7 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
       if (P.fp8) decode_tile<D, 0>(raw, params, ln, live, dst);
-      else if (bits == 8) decode_tile<D, 8>(raw, params, ln, live, dst);
+      else if (bits == 8)
+        decode_tile<D, 8>(raw, reinterpret_cast<const uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
+                                   ((static_cast<int64_t>(ms->raw_block[e]) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
+                                       (D / kGroup * 4),
+                          ln, live, dst);
       else if (bits == 2) decode_tile<D, 2>(raw, params, ln, live, dst);
       else decode_tile<D, 4>(raw, params, ln, live, dst);
       fence_async_shared();
@@ -568,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
   } else {
     regs_up<kSoftRegs>();
-    if ((warp & 3) < (group == 0 ? warps0 : warps1)) {
+    if (group < 2 && (warp & 3) < (group == 0 ? warps0 : warps1)) {
       // ---- softmax -------------------------------------------------------------
       const int local = (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
       const int r = w.r0 + local;
@@ -589,16 +593,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       auto token = [&](int k) {
         return w.t0 + (MODE == 1 ? (2 * (k / G::STEPS) + group) * BN + k % G::STEPS * kCols : k * kCols);
       };
-      float m = -INFINITY, l = 0.0f;
+      float m = kNone, l = 0.0f;
       bool poison = false;
-      for (int k = 0; k < steps; ++k) {
-        const uint32_t s_at = tmem + lanes + kSBase + group * (2 * kCols) + (k & 1) * kCols;
+      const float2 rs2 = make_float2(rs, rs);
+      uint64_t* turn = &ms->turn[group][warp & 3];
+      float* reference = &ms->reference[group * 128 + (warp & 3) * 32 + lane];
+      const uint32_t s_at = tmem + lanes + kSBase + group * (2 * kCols) + side * kCols;
+
+#pragma unroll 1
+      for (int k = side; k < steps; k += 2) {
         const int t0 = token(k);
         const int hi = pos - t0;                           // last column the row sees
         const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
-        warp_wait(&ms->s_full[group][k & 1], (k >> 1) & 1, ms);
-        tc_fence_after();
         uint32_t x[2][32];
+        warp_wait(&ms->s_full[group][side], (k >> 1) & 1, ms);
+        tc_fence_after();
         tmem_ld32(s_at, x[0]);
         tmem_ld32(s_at + 32, x[1]);
         // (the key decoders wrote this before the tile that the logits come from)
@@ -633,50 +642,62 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
           for (int q = 0; q < 4; ++q)
             mx[q] = max3(mx[q], __uint_as_float(x[q & 1][i + (q >> 1)]), __uint_as_float(x[q & 1][i + 2 + (q >> 1)]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * rs;
-        if (__any_sync(0xffffffffu, real && top > m + kLazy)) {
-          // Move the reference: it stays a whole number, so everything scaled
-          // by it scales by a power of two.
-          const float to = ceilf(fmaxf(m, top));
-          const float f = to == -INFINITY ? 1.0f : __int_as_float((static_cast<int>(fmaxf(m - to, -127.0f)) + 127) << 23);
-          m = to;
-          l *= f;
+        // the reference after the step before, which the other group settles
+        float ref = kNone;
+        if (k > 0) {
+          warp_wait(turn, (k - 1) & 1, ms);
+          ref = *reinterpret_cast<volatile float*>(reference);
+        }
+        if (__any_sync(0xffffffffu, real && top > ref + kLazy)) {
+          // Move it: it stays a whole number, so everything scaled by it scales
+          // by a power of two.
+          const float to = fmaxf(ceilf(fmaxf(ref, top)), kNone);
           if (k > 0) {
-            warp_wait(&ms->o_done[group][(k - 1) & 1], ((k - 1) >> 1) & 1, ms);
+            const float f = __int_as_float((static_cast<int>(fmaxf(ref - to, -127.0f)) + 127) << 23);
+            warp_wait(&ms->o_done[group][side ^ 1], ((k - 1) >> 1) & 1, ms);
             tc_fence_after();
 #pragma unroll 1
-            for (int e = 0; e < D / 16; ++e) {
-              uint32_t o[16];
-              tmem_ld16(o_at + 16 * e, o);
+            for (int e = 0; e < D / 8; ++e) {
+              uint32_t o[8];
+              tmem_ld8(o_at + 8 * e, o);
               tmem_wait_ld(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(o_at + 16 * e, o);
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st8(o_at + 8 * e, o);
             }
           }
+          ref = to;
         }
-        const float off = kShift - (m == -INFINITY ? 0.0f : m);
-        const float2 rs2 = make_float2(rs, rs), off2 = make_float2(off, off);
+        if (k == 0 || ref != m) *reinterpret_cast<volatile float*>(reference) = ref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(turn);
+        l *= exp2_fast(m - ref);                           // (the group's sum goes by the reference it last saw)
+        m = ref;
+        const float2 off2 = make_float2(kShift - m, kShift - m);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
+        for (int c = 0; c < 8; ++c) {
+          uint32_t p[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), rs2, off2);
+          for (int i = 0; i < 4; ++i) {
+            const int at = 4 * c + i;
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[at >> 4][(2 * at) & 31]), __uint_as_float(x[at >> 4][(2 * at + 1) & 31])),
+                                        rs2, off2);
             const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum[i & 1] = __fadd2_rn(sum[i & 1], q);
             p[i] = h2u(__floats2half2_rn(q.x, q.y));
           }
-          tmem_st16(s_at + 16 * c, p);
+          tmem_st4(s_at + 4 * c, p);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->p_full[group][k & 1]);
+        if (lane == 0) mbar_arrive(&ms->p_full[group][side]);
       }
-
-      if (steps > 0) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, ms);
+      // The last product: the group that made its weights has seen the product
+      // two before it, as a wait on that barrier has to.
+      if (steps > 0 && ((steps - 1) & 1) == side) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, ms);
       result.m = m;
       result.l = l;
       result.poison = poison;
@@ -684,29 +705,40 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
   }
   tc_fence_before();
-  __syncthreads();         // every product is done: the tiles' place is free
+  __syncthreads();         // every product is done: the places of the tiles, packed and decoded, are free
   tc_fence_after();
+  // what the groups of the same rows have, in the packed tiles' place
+  float4* told = reinterpret_cast<float4*>(sm + G::kRawAt);
+  const int place = (group * 2 + side) * 128 + (warp & 3) * 32 + lane;
+  const bool mine_real = warp < kDecodeWarp0 && group < 2 && (warp & 3) < (group == 0 ? warps0 : warps1);
+  if (mine_real) told[place] = make_float4(result.m, result.l, result.poison ? 1.0f : 0.0f, 0.0f);
+  __syncthreads();
 
-  if (warp < 8 && (warp & 3) < (group == 0 ? warps0 : warps1)) {
-    // ---- result ----------------------------------------------------------------
-    // A warp's 32 rows go through shared memory, 16 bytes a lane and swizzled by
-    // the row, so that every store to global memory is of whole rows.
+  // ---- result ------------------------------------------------------------------
+  // The rows go through shared memory, 16 bytes a lane and swizzled by the row,
+  // and every warp then writes whole rows.
+  const bool wide = partials > 1 || a.out_dtype == Q4KV_F32;
+  const int pieces = wide ? D / 4 : D / 8;                 // 16-byte pieces of a row
+  const int64_t part = static_cast<int64_t>(w.split) * G::STREAMS * all_rows;
+  uint8_t* stage = sm + G::kQ;
+  if (mine_real) {
     const bool ok = ms->abort == 0;
-    const int first = w.r0 + (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32, r = first + lane;
+    const float4 other = told[place ^ 128];
+    const float top = fmaxf(result.m, other.x);            // (references only grow: the last one)
+    result.l = result.l * exp2_fast(result.m - top) + other.y * exp2_fast(other.x - top);
+    result.m = top;
+    result.poison = result.poison || other.z != 0.0f;
+    const int r = w.r0 + (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
     const bool fine = ok && !result.poison && result.l > 0.0f;
-    const int64_t part = static_cast<int64_t>(w.split * G::STREAMS + (MODE == 1 ? group : 0)) * all_rows;
-    auto row_of = [&](int q) {                             // (sequence, token, head) of tile row q
-      return (static_cast<int64_t>(w.b) * w.T + q / w.g) * hq + w.h * w.g + q % w.g;
-    };
-    if (partials > 1 && r < w.rv) a.ws_ml[part + row_of(r)] = make_float2(ok ? result.m : 0.0f, ok && !result.poison ? result.l : -1.0f);
+    if (partials > 1 && r < w.rv && side == 0)
+      a.ws_ml[part + (MODE == 1 ? group : 0) * all_rows + (static_cast<int64_t>(w.b) * w.T + r / w.g) * hq + w.h * w.g + r % w.g] =
+          make_float2(!ok ? 0.0f : result.l > 0.0f ? result.m : -INFINITY, ok && !result.poison ? result.l : -1.0f);
     if (result.any) {
-      const bool wide = partials > 1 || a.out_dtype == Q4KV_F32;
-      const int pieces = wide ? D / 4 : D / 8;             // 16-byte pieces of a row
-      uint8_t* stage = sm + G::kQ + warp * (32 * D * 4);
       const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 128;
       const float f = partials > 1 ? 1.0f : (fine ? 1.0f / result.l : 0.0f);
+      uint8_t* mine = stage + (group * 128 + (warp & 3) * 32 + lane) * (pieces * 16);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = side * (D / 64); c < (side + 1) * (D / 64); ++c) {
         uint32_t x[32];
         float y[32];
         tmem_ld32(o_at + 32 * c, x);
@@ -716,7 +748,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = 0.0f;
         }
-        uint8_t* mine = stage + lane * (pieces * 16);
         if (wide) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -729,24 +760,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                            pack16(a.out_dtype, y[8 * e + 4], y[8 * e + 5]), pack16(a.out_dtype, y[8 * e + 6], y[8 * e + 7]));
         }
       }
-      __syncwarp();
-      const int rows = min(32, w.rv - first);
-      for (int x = lane; x < rows * pieces; x += 32) {
-        const int q = x / pieces, e = x % pieces;
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + q * (pieces * 16) + (e ^ (q & 7)) * 16);
-        const int rq = first + q;
-        if (partials > 1) {
-          *reinterpret_cast<uint4*>(a.ws_o + (part + row_of(rq)) * D + e * 4) = v;
-        } else {
-          const int64_t at = w.b * a.o_seq_stride + (rq / w.g) * a.o_token_stride + static_cast<int64_t>(w.h * w.g + rq % w.g) * D;
-          if (wide) *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at + e * 4) = v;
-          else *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + at + e * 8) = v;
-        }
-      }
     }
     tc_fence_before();
   }
   __syncthreads();
+  {
+    const int rows = w.rv - w.r0;
+    for (int x = warp; x < (MODE == 1 && steps1 > 0 ? 2 : 1) * rows; x += kThreads / 32) {
+      const int s = MODE == 1 && x >= rows ? 1 : 0, q = x - s * rows, r = w.r0 + q;
+      const int i = r / w.g, head = w.h * w.g + r % w.g;
+      uint8_t* dst;
+      if (partials > 1) dst = reinterpret_cast<uint8_t*>(a.ws_o + (part + s * all_rows + (static_cast<int64_t>(w.b) * w.T + i) * hq + head) * D);
+      else dst = static_cast<uint8_t*>(a.out) + (w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D) * (wide ? 4 : 2);
+      const uint8_t* src = stage + (MODE == 1 ? s * 128 + q : q) * (pieces * 16);
+      for (int e = lane; e < pieces; e += 32)
+        reinterpret_cast<uint4*>(dst)[e] = *reinterpret_cast<const uint4*>(src + (e ^ (q & 7)) * 16);
+    }
+  }
   if (tid == 0 && ms->abort != 0) raise_error(P.error_word, Q4KV_DEVERR_TIMEOUT);
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -821,8 +851,8 @@ cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
   const int64_t group_rows = static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads);
   const int64_t x = (group_rows + G::R - 1) / G::R * p.n_splits;
   if (x > 0x7fffffff) return cudaErrorInvalidValue;
-  const uint32_t codes = G::BN * G::D / 8 * (a.pool.n_q8 > 0 ? 8 : 4);
-  const uint32_t stride = codes + G::BN * (G::D / kGroup) * 4 + 16;
+  // packed codes, scales (except for 8-bit codes) and mask
+  const uint32_t stride = a.pool.n_q8 > 0 ? G::BN * G::D + 16 : G::BN * G::D / 2 + G::BN * (G::D / kGroup) * 4 + 16;
   const int n_raw = min(kMaxRaw, static_cast<int>(G::kRawRing / stride));
   constexpr uint32_t kSmem = smem_bytes<MODE>();
   cudaFuncAttributes attr;

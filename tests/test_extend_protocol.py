@@ -1,11 +1,12 @@
 """Event model of the chunk-attention kernel's barriers (CPU).
 
-The kernel's roles (feed, key and value decoders, product, softmax groups) meet
-at mbarriers and wait by phase parity, which tells only two neighbouring phases
+The kernel's roles (feed, key and value decoders, product, softmax groups by
+turns) meet at mbarriers and wait by phase parity, which tells only two neighbouring phases
 of a barrier apart.  Here the roles run in random order, copies land in random
 order and products finish in issue order; every use of a buffer checks that it
 holds what its user expects.  As controls, barriers shared by keys and values
-(with an odd number of places) and one barrier for both logit buffers fail."""
+(with an odd number of places), one barrier for both logit buffers and a wait for
+the last product by the group that has not seen the one two before it fail."""
 import random
 
 import pytest
@@ -25,14 +26,15 @@ class Bar:
         return (self.done & 1) != parity
 
 
-def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False):
-    """mode 0: groups with rows of their own; 1: groups on alternate tiles; 2: one step a tile."""
+def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False, all_wait=False):
+    """mode 0: accumulators with rows of their own; 1: on alternate tiles; 2: one step a tile."""
     r = random.Random(seed)
     per = 1 if mode == 2 else 2                # softmax steps of a tile
     k_raw, k_slot = (n_raw, slots) if shared else (2 * n_raw, 2 * slots)
     raw_full, raw_empty = [Bar(1) for _ in range(k_raw)], [Bar(4) for _ in range(n_raw)]
     kv_full, kv_empty = [Bar(4) for _ in range(slots)], [Bar(1) for _ in range(k_slot)]
     s_full, p_full, o_done = ([[Bar(1), Bar(1)] for _ in range(2)] for _ in range(3))
+    turn, settled = [Bar(1), Bar(1)], [-1, -1]  # the last step whose reference is known
     raw, slot = [None] * n_raw, [(None, 0)] * slots
     logits = [[None, None], [None, None]]      # what each buffer holds: ("S" or "P", step)
     flying, queue = [], []
@@ -94,27 +96,36 @@ def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False):
                     queue.append(("qk", s, u, i, last))
                     yield
 
-    def softmax(s):
+    def softmax(s, side):
         def done(k):
             return o_done[s][0].ready(k & 1) if one_done else o_done[s][k & 1].ready((k >> 1) & 1)
 
-        for k in range(steps[s]):
-            while not s_full[s][k & 1].ready((k >> 1) & 1):
+        for k in range(side, steps[s], 2):
+            while not s_full[s][side].ready((k >> 1) & 1):
                 yield
-            assert logits[s][k & 1] == ("S", k), "logits"
+            assert logits[s][side] == ("S", k), "logits"
+            while k and not turn[s].ready((k - 1) & 1):
+                yield
+            assert settled[s] == k - 1, "reference"
             if k and r.random() < 0.5:         # the maximum moves: the accumulator is rescaled
                 while not done(k - 1):
                     yield
                 assert k - 1 in products[s], "accumulator not ready"
+                assert max(products[s]) == k - 1, "accumulator moved on"
             yield
-            logits[s][k & 1] = ("P", k)
-            p_full[s][k & 1].arrive()
+            settled[s] = k
+            turn[s].arrive()
             yield
-        while steps[s] and not done(steps[s] - 1):
+            assert logits[s][side] == ("S", k), "logits"
+            logits[s][side] = ("P", k)
+            p_full[s][side].arrive()
             yield
-        assert not steps[s] or steps[s] - 1 in products[s], "result read too early"
+        if steps[s] and (all_wait or (steps[s] - 1) & 1 == side):
+            while not done(steps[s] - 1):
+                yield
+            assert steps[s] - 1 in products[s], "result read too early"
 
-    roles = [feed(), product()] + [softmax(s) for s in range(groups)] + [decoder(k) for k in (0, 1) for _ in range(4)]
+    roles = [feed(), product()] + [softmax(s, side) for s in range(groups) for side in (0, 1)] + [decoder(k) for k in (0, 1) for _ in range(4)]
     idle = 0
     while roles:
         x = r.random()
@@ -157,10 +168,10 @@ def test_roles_never_meet_a_wrong_buffer(mode, groups, n_raw):
             run(mode, groups, n_raw, n, seed)
 
 
-@pytest.mark.parametrize("kw", [{"shared": True, "slots": 3}, {"shared": True, "n_raw": 3}, {"one_done": True}])
+@pytest.mark.parametrize("kw", [{"shared": True, "slots": 3}, {"shared": True, "n_raw": 3}, {"one_done": True}, {"all_wait": True}])
 def test_controls_fail(kw):
     failed, n_raw = 0, kw.get("n_raw", 3)
-    for seed in range(80):
+    for seed in range(200):
         try:
             run(2, 1, n_raw, 17, seed, **{k: v for k, v in kw.items() if k != "n_raw"})
         except AssertionError:
