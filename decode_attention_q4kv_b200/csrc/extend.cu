@@ -365,35 +365,41 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     using Sh = Shape<D>;
     constexpr int kPasses = G::R / Sh::VPW / 16;           // of a warp
     const int rl = lane / Sh::LPV, j = lane % Sh::LPV;
-    uint4 in[kPasses][2];
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
+    // (a warp's passes lie 16 apart; the next one's row is on its way meanwhile)
+    auto load = [&](int p, uint4 (&in)[2]) {
       const int rr = w.r0 + (p * 16 + warp) * Sh::VPW + rl;
-      in[p][0] = in[p][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < w.rv) {
+      in[0] = in[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (p < kPasses && rr < w.rv) {
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __half*>(a.q) + w.b * a.q_seq_stride + (rr / w.g) * a.q_token_stride +
             static_cast<int64_t>(w.h * w.g + rr % w.g) * D + j * kEPL);
-        in[p][0] = __ldg(src);
-        in[p][1] = __ldg(src + 1);
+        in[0] = __ldg(src);
+        in[1] = __ldg(src + 1);
       }
-    }
-    __syncwarp();
-#pragma unroll
+    };
+    uint4 in[2], next[2];
+    load(0, next);
+#pragma unroll 1
     for (int p = 0; p < kPasses; ++p) {
       const int row = (p * 16 + warp) * Sh::VPW + rl;
       if (w.r0 + (p * 16 + warp) * Sh::VPW >= w.rv) break; // (the whole warp)
+      in[0] = next[0];
+      in[1] = next[1];
+      load(p + 1, next);
+      __syncwarp();
       float2 x[8];
-      if (a.q_dtype == Q4KV_F16) unpack16<__half>(in[p][0], in[p][1], x);
-      else unpack16<__nv_bfloat16>(in[p][0], in[p][1], x);
+      if (a.q_dtype == Q4KV_F16) unpack16<__half>(in[0], in[1], x);
+      else unpack16<__nv_bfloat16>(in[0], in[1], x);
       if (P.k_rotated) {
         rotate_pairs<D>(x, j);
+        if (kRotScale<D> != 1.0f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x * kRotScale<D>, x[i].y * kRotScale<D>);
+          for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x * kRotScale<D>, x[i].y * kRotScale<D>);
+        }
       }
       float m = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+      for (int i = 0; i < 8; ++i) m = max3(m, fabsf(x[i].x), fabsf(x[i].y));
 #pragma unroll
       for (int st = 1; st < Sh::LPV; st <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, st));
       // the row's largest magnitude comes to lie in [64, 128)
@@ -467,42 +473,54 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     } else if (warp == kMmaWarp) {
       // ---- product -------------------------------------------------------------
       if (elect_one()) {
-        constexpr uint32_t kQk = mma_f16_desc(128, kCols, false), kPv = mma_f16_desc(128, D, true);
+        constexpr uint32_t kQk = mma_f16_desc(128, BN, false), kPv = mma_f16_desc(128, D, true);
         const uint64_t q0 = smem_operand(smem_u32(sm), 16, 1024), k0 = smem_operand(smem_u32(sm) + G::kQ, 16, 1024),
                        v0 = smem_operand(smem_u32(sm) + G::kQ, BN * 128, 1024);
-        for (int u = 0; u < steps0 + 2; ++u) {
-          for (int s = 0; s < groups; ++s) {
-            const int steps = s == 0 ? steps0 : steps1;
-            const uint32_t logits = tmem + kSBase + s * (2 * kCols) + (u & 1) * kCols;   // of steps u - 2 and u
-            const int v = u - 2;
-            if (v >= 0 && v < steps) {                     // O += P V
-              const int j = MODE == 1 ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
-              wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
-              wait(&ms->p_full[s][v & 1], (v >> 1) & 1, ms);
-              tc_fence_after();
-              const uint64_t vd = v0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
+        // O += P V of step v of accumulator s
+        auto pv = [&](int s, int v) {
+          const int j = MODE == 1 ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
+          if (h == 0 && (MODE != 0 || s == 0)) wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);   // first use
+          wait(&ms->p_full[s][v & 1], (v >> 1) & 1, ms);
+          tc_fence_after();
+          const uint32_t p = tmem + kSBase + s * (2 * kCols) + (v & 1) * kCols;
+          const uint64_t vd = v0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
 #pragma unroll
-              for (int k = 0; k < kCols / 16; ++k) mma_ts(tmem + s * 128, logits + k * 8, vd + k * (2048 >> 4), kPv, v > 0 || k > 0);
-              mma_commit(&ms->o_done[s][v & 1]);
-              if (h == G::STEPS - 1 && (MODE != 0 || s == groups - 1)) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
-            }
-            if (u < steps) {                               // S = Q K^T
-              const int j = MODE == 1 ? 2 * (u / G::STEPS) + s : u / G::STEPS, h = u % G::STEPS, n = 2 * j;
-              wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
-              tc_fence_after();
-              const uint64_t qd = q0 + (MODE == 0 ? s * (128 * D * 2 >> 4) : 0);
-              const uint64_t kd = k0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
-              // (the product that read the weights in this buffer was issued
-              // before this one; products of one thread run in order)
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_ss(logits, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                       kd + (((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4), kQk, k > 0);
-              mma_commit(&ms->s_full[s][u & 1]);
-              if (h == G::STEPS - 1 && (MODE != 0 || s == groups - 1)) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
-            }
+          for (int k = 0; k < kCols / 16; ++k) mma_ts(tmem + s * 128, p + k * 8, vd + k * (2048 >> 4), kPv, v > 0 || k > 0);
+          mma_commit(&ms->o_done[s][v & 1]);
+          if (h == G::STEPS - 1 && (MODE != 0 || s == groups - 1)) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
+        };
+        // S = Q K^T of accumulator s's tile i.  (The products that read the
+        // weights in these buffers were issued before; products of one thread
+        // run in order.)
+        auto qk = [&](int s, int i) {
+          const int j = MODE == 1 ? 2 * i + s : i, n = 2 * j;
+          if (MODE != 0 || s == 0) {
+            wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
+            tc_fence_after();
           }
-        }
+          const uint64_t qd = q0 + (MODE == 0 ? s * (128 * D * 2 >> 4) : 0), kd = k0 + ((n % kSlots) * kTile >> 4);
+          const uint32_t logits = tmem + kSBase + s * (2 * kCols) + (G::STEPS == 1 ? (i & 1) * kCols : 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(logits, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), kd + (((k >> 2) * (BN * 128) + (k & 3) * 32) >> 4), kQk,
+                   k > 0);
+          if (G::STEPS == 1) {
+            mma_commit(&ms->s_full[s][i & 1]);
+          } else {
+            mma_commit(&ms->s_full[s][0]);
+            mma_commit(&ms->s_full[s][1]);
+          }
+          if (MODE != 0 || s == groups - 1) mma_commit(&ms->kv_empty[n % (2 * kSlots)]);
+        };
+        // logits of a tile of 128 tokens fill both buffers; of 64, one of two
+        constexpr int kAhead = G::STEPS == 1 ? 2 : 1;
+        for (int i = 0; i < steps0 / G::STEPS + kAhead; ++i)
+          for (int s = 0; s < groups; ++s) {
+            const int tiles = (s == 0 ? steps0 : steps1) / G::STEPS;
+            if (i >= kAhead && i - kAhead < tiles)
+              for (int h = 0; h < G::STEPS; ++h) pv(s, (i - kAhead) * G::STEPS + h);
+            if (i < tiles) qk(s, i);
+          }
         if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) {    // let the products in flight end
           mma_commit(&ms->spare);
           mbar_wait(&ms->spare, 0);
@@ -614,23 +632,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         const int j = MODE == 1 ? 2 * (k / G::STEPS) + group : k / G::STEPS;
         const uint2 gone = *reinterpret_cast<const uint2*>(&ms->gone[j & 7][2 * (k % G::STEPS)]);
         const bool bad = ms->bad[j & 7] != 0;
-        const bool plain = pos_first - t0 >= kCols - 1 && (a.plan.window == 0 || pos_last - a.plan.window < t0) &&
-                           (gone.x | gone.y) == 0 && !bad;
+        const bool edge = pos_first - t0 < kCols - 1 || (a.plan.window != 0 && pos_last - a.plan.window >= t0);
         tmem_wait_ld(x[0]);
         tmem_wait_ld(x[1]);
         if (bad && hi >= 0 && lo < kCols) poison = true;
-        if (!plain) {
+        if ((gone.x | gone.y) != 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if ((gone.x >> i) & 1u) x[0][i] = __float_as_uint(sent);
+            if ((gone.y >> i) & 1u) x[1][i] = __float_as_uint(sent);
+          }
+        }
+        if (edge) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int h1 = hi - 32 * c, l1 = lo - 32 * c;
             uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
             seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
-            const uint32_t away = c == 0 ? gone.x : gone.y;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = (away >> i) & 1u ? sent : __uint_as_float(x[c][i]);
-              x[c][i] = __float_as_uint((seen >> i) & 1u ? y : -INFINITY);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (!((seen >> i) & 1u)) x[c][i] = __float_as_uint(-INFINITY);
           }
         }
         float mx[4];

@@ -39,7 +39,7 @@ def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False, all
     logits = [[None, None], [None, None]]      # what each buffer holds: ("S" or "P", step)
     flying, queue = [], []
     products = [set(), set()]
-    uses = {i: per * (groups if mode == 0 else 1) for i in range(2 * n)}
+    uses = {i: (per if i & 1 else 1) * (groups if mode == 0 else 1) for i in range(2 * n)}
     steps = [((n - s + 1) // 2 if mode == 1 else n) * per for s in range(groups)]
 
     def tile(s, k):
@@ -73,27 +73,29 @@ def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False, all
             yield
 
     def product():
-        for u in range(steps[0] + 2):
+        ahead = 2 if per == 1 else 1
+        for i in range(steps[0] // per + ahead):
             for s in range(groups):
-                v = u - 2
-                if 0 <= v < steps[s]:
-                    i = 2 * tile(s, v) + 1
-                    while not kv_full[i % slots].ready((i // slots) & 1):
+                tiles = steps[s] // per
+                if i >= ahead and i - ahead < tiles:
+                    for h in range(per):
+                        v = (i - ahead) * per + h
+                        n_ = 2 * tile(s, v) + 1
+                        while h == 0 and not kv_full[n_ % slots].ready((n_ // slots) & 1):
+                            yield
+                        assert slot[n_ % slots] == (n_, 4), "values"
+                        while not p_full[s][v & 1].ready((v >> 1) & 1):
+                            yield
+                        assert logits[s][v & 1] == ("P", v), "weights"
+                        last = h == per - 1 and (mode != 0 or s == groups - 1)
+                        queue.append(("pv", s, v, n_, last))
                         yield
-                    assert slot[i % slots] == (i, 4), "values"
-                    while not p_full[s][v & 1].ready((v >> 1) & 1):
+                if i < tiles:
+                    n_ = 2 * tile(s, i * per)
+                    while not kv_full[n_ % slots].ready((n_ // slots) & 1):
                         yield
-                    assert logits[s][v & 1] == ("P", v), "weights"
-                    last = v % per == per - 1 and (mode != 0 or s == groups - 1)
-                    queue.append(("pv", s, v, i, last))
-                    yield
-                if u < steps[s]:
-                    i = 2 * tile(s, u)
-                    while not kv_full[i % slots].ready((i // slots) & 1):
-                        yield
-                    assert slot[i % slots] == (i, 4), "keys"
-                    last = u % per == per - 1 and (mode != 0 or s == groups - 1)
-                    queue.append(("qk", s, u, i, last))
+                    assert slot[n_ % slots] == (n_, 4), "keys"
+                    queue.append(("qk", s, i, n_, mode != 0 or s == groups - 1))
                     yield
 
     def softmax(s, side):
@@ -140,8 +142,9 @@ def run(mode, groups, n_raw, n, seed, slots=4, shared=False, one_done=False, all
             assert slot[i % slots][0] == i, "operand overwritten"
             uses[i] -= 1
             if what == "qk":
-                logits[s][u & 1] = ("S", u)
-                s_full[s][u & 1].arrive()
+                for v in range(u * per, (u + 1) * per):
+                    logits[s][v & 1] = ("S", v)
+                    s_full[s][v & 1].arrive()
             else:
                 assert logits[s][u & 1] == ("P", u), "weights overwritten"
                 products[s].add(u)
