@@ -56,6 +56,43 @@ def _require_cuda(*ts: torch.Tensor) -> torch.device:
     return dev
 
 
+# Helpers of the calls that a server makes every step, kept short: on the
+# smallest ones the host's work is what takes the time.
+
+def _same_device(*ts: Optional[torch.Tensor]) -> int:
+    """Index of the one CUDA device all the tensors are on."""
+    dev = -1
+    for t in ts:
+        if t is not None:
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("q4kv works on CUDA tensors only")
+            if dev < 0:
+                dev = i
+            elif i != dev:
+                raise ValueError("all tensors must be on one device")
+    return dev
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _int32(t: torch.Tensor) -> torch.Tensor:
+    return t if t.dtype is torch.int32 and t.is_contiguous() else t.to(torch.int32).contiguous()
+
+
+def _call(dev: int, name: str, *args) -> None:
+    """One library call on a device's current stream (its last argument)."""
+    if torch.cuda.current_device() == dev:
+        status = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if status:
+        check(status, name)
+
+
 class Q4KVPool:
     """Device storage of the paged cache plus its C descriptor.
 
@@ -121,6 +158,7 @@ class Q4KVPool:
             self.v_codes2.data_ptr() if n_q2_blocks else 0,
             self.k_params2.data_ptr() if n_q2_blocks else 0,
             self.v_params2.data_ptr() if n_q2_blocks else 0)
+        self._ref = ctypes.byref(self.desc)
 
     @classmethod
     def from_tensors(cls, n_kv_heads: int, head_dim: int, mask: torch.Tensor, k_rotated: bool = True,
@@ -229,40 +267,41 @@ class Q4KVPool:
         q [B][T][Hq][D] are rotated along and returned (rows at or past
         n_new[b] are 0).  positions is [n_axes][B][T]; None places token i of
         sequence b at seq_lens[b] + i on every axis.  q_out may be q."""
-        dev = _require_cuda(self.mask, k, v, tables, seq_lens, n_new, positions, q, q_out, rotary.table)
+        dev = _same_device(self.mask, k, v, tables, seq_lens, n_new, positions, q, q_out, rotary.table)
         _check_chunk(k, "k")
-        _check_chunk(v, "v")
-        if k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride():
-            raise ValueError("k and v must share dtype, shape and strides")
         B, T, hkv, d = k.shape
-        if (hkv, d) != (self.n_kv_heads, self.head_dim):
+        ks = k.stride()
+        if v.dtype != k.dtype or v.shape != k.shape or v.stride() != ks:
+            raise ValueError("k and v must share dtype, shape and strides")
+        if hkv != self.n_kv_heads or d != self.head_dim:
             raise ValueError(f"k and v must have {self.n_kv_heads} heads of {self.head_dim}")
         tab, lens, nn = _sequences(B, tables, seq_lens, n_new)
         pos = None
         if positions is not None:
             if tuple(positions.shape) != (rotary.desc.n_axes, B, T):
                 raise ValueError(f"positions must be [{rotary.desc.n_axes}][B][T]")
-            pos = positions.to(torch.int32).contiguous()
+            pos = _int32(positions)
         hq, qs, os_ = 0, (0, 0), (0, 0)
         if q is not None:
             _check_chunk(q, "q")
             hq = q.shape[2]
-            if q.dtype != k.dtype or tuple(q.shape) != (B, T, hq, d):
+            if q.dtype != k.dtype or q.shape != (B, T, hq, d):
                 raise ValueError("q must be [B][T][Hq][D] of the keys' dtype")
             if q_out is None:
-                q_out = torch.empty((B, T, hq, d), dtype=q.dtype, device=dev)
-            _check_chunk(q_out, "q_out")
-            if q_out.shape != q.shape or q_out.dtype != q.dtype:
-                raise ValueError("q_out must have q's shape and dtype")
-            qs, os_ = _row_strides(q), _row_strides(q_out)
+                q_out = torch.empty((B, T, hq, d), dtype=q.dtype, device=q.device)
+                os_ = (T * hq * d, hq * d)
+            else:
+                _check_chunk(q_out, "q_out")
+                if q_out.shape != q.shape or q_out.dtype != q.dtype:
+                    raise ValueError("q_out must have q's shape and dtype")
+                os_ = _row_strides(q_out)
+            qs = _row_strides(q)
         elif q_out is not None:
             raise ValueError("q_out without q")
         ks = _row_strides(k)
-        with torch.cuda.device(dev):
-            check(lib().q4kv_append_rotary(
-                ctypes.byref(self.desc), ctypes.byref(rotary.desc), _ptr(k), _ptr(v), _IN_DTYPES[k.dtype], B, T, _ptr(nn),
-                ks[0], ks[1], _ptr(q), hq, qs[0], qs[1], _ptr(q_out), os_[0], os_[1], _ptr(tab), tab.shape[1],
-                _ptr(lens), _ptr(pos), _stream(dev)), "q4kv_append_rotary")
+        _call(dev, "q4kv_append_rotary", self._ref, rotary._ref, k.data_ptr(), v.data_ptr(), _IN_DTYPES[k.dtype], B, T,
+              _addr(nn), ks[0], ks[1], _addr(q), hq, qs[0], qs[1], _addr(q_out), os_[0], os_[1], tab.data_ptr(),
+              tab.shape[1], lens.data_ptr(), _addr(pos))
         return q_out
 
     def invalidate(self, slot_ids: torch.Tensor) -> None:
@@ -343,30 +382,31 @@ class Q4KVPool:
         starts[b] (None = 0) on, found through tables [B][max_blocks].  Rows
         that no sequence covers are left as they were (undefined where this
         call allocates the outputs).  Remapped slots read K = -1e4, V = 0."""
-        dev = _require_cuda(self.mask, tables, starts, offsets, k_out, v_out)
+        dev = _same_device(self.mask, tables, starts, offsets, k_out, v_out)
         B = tables.shape[0]
-        if tables.dim() != 2 or tuple(offsets.shape) != (B + 1,) or (starts is not None and tuple(starts.shape) != (B,)):
+        if tables.dim() != 2 or offsets.shape != (B + 1,) or (starts is not None and starts.shape != (B,)):
             raise ValueError("tables must be [B][max_blocks], offsets [B+1] and starts [B]")
         if out_dtype not in _OUT_DTYPES:
             raise ValueError("out_dtype must be float32, float16 or bfloat16")
         shape = (int(n_rows), self.n_kv_heads, self.head_dim)
-        outs = []
+        stride = shape[1] * shape[2]
         for o, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if o is None:
-                o = torch.empty(shape, dtype=out_dtype, device=dev)
-            elif tuple(o.shape) != shape or o.dtype != out_dtype or o.stride(2) != 1 or o.stride(1) != shape[2]:
+            if o is not None and (tuple(o.shape) != shape or o.dtype != out_dtype or o.stride(2) != 1 or o.stride(1) != shape[2]):
                 raise ValueError(f"{name} must be {out_dtype} of shape {shape} with contiguous rows")
-            outs.append(o)
-        if shape[0] > 1 and outs[0].stride(0) != outs[1].stride(0):
-            raise ValueError("k_out and v_out must have equal strides")
-        stride = outs[0].stride(0) if shape[0] > 1 else shape[1] * shape[2]
-        tab, off = tables.to(torch.int32).contiguous(), offsets.to(torch.int32).contiguous()
-        st = None if starts is None else starts.to(torch.int32).contiguous()
-        with torch.cuda.device(dev):
-            check(lib().q4kv_gather_tokens(ctypes.byref(self.desc), _ptr(tab), tab.shape[1], B, _ptr(st), _ptr(off),
-                                           shape[0], _ptr(outs[0]), _ptr(outs[1]), stride, _OUT_DTYPES[out_dtype],
-                                           int(unrotate_k), _stream(dev)), "q4kv_gather_tokens")
-        return outs[0], outs[1]
+        if shape[0] > 1:
+            given = [o.stride(0) for o in (k_out, v_out) if o is not None]
+            if len(set(given)) > 1 or (len(given) == 1 and given[0] != stride):
+                raise ValueError("k_out and v_out must have equal strides")
+            stride = given[0] if given else stride
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=out_dtype, device=tables.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=out_dtype, device=tables.device)
+        tab, off = _int32(tables), _int32(offsets)
+        st = None if starts is None else _int32(starts)
+        _call(dev, "q4kv_gather_tokens", self._ref, tab.data_ptr(), tab.shape[1], B, _addr(st), off.data_ptr(), shape[0],
+              k_out.data_ptr(), v_out.data_ptr(), stride, _OUT_DTYPES[out_dtype], int(unrotate_k))
+        return k_out, v_out
 
     def read_device_error(self, clear: bool = True) -> int:
         """Synchronise the current stream and return the device error bits."""
@@ -381,24 +421,24 @@ class Q4KVPool:
 def _check_chunk(x: torch.Tensor, name: str) -> None:
     if x.dtype not in _IN_DTYPES or x.dim() != 4:
         raise ValueError(f"{name} must be float16 or bfloat16 [B][T][H][D]")
-    if x.stride(3) != 1 or x.stride(2) != x.shape[3]:
+    s = x.stride()
+    if s[3] != 1 or s[2] != x.shape[3]:
         raise ValueError(f"each token's [H][D] row of {name} must be contiguous")
 
 
 def _row_strides(x: torch.Tensor) -> Tuple[int, int]:
     """Sequence and token stride in elements; an axis of one entry has no stride of its own."""
-    row = x.shape[2] * x.shape[3]
-    token = x.stride(1) if x.shape[1] > 1 else row
-    return (x.stride(0) if x.shape[0] > 1 else token * max(x.shape[1], 1)), token
+    (B, T, H, D), s = x.shape, x.stride()
+    token = s[1] if T > 1 else H * D
+    return (s[0] if B > 1 else token * max(T, 1)), token
 
 
 def _sequences(B: int, tables: torch.Tensor, seq_lens: torch.Tensor, n_new: Optional[torch.Tensor]):
-    if tables.dim() != 2 or tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
+    if tables.dim() != 2 or tables.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("tables must be [B][max_blocks] and seq_lens [B]")
-    if n_new is not None and tuple(n_new.shape) != (B,):
+    if n_new is not None and n_new.shape != (B,):
         raise ValueError("n_new must be [B]")
-    return (tables.to(torch.int32).contiguous(), seq_lens.to(torch.int32).contiguous(),
-            None if n_new is None else n_new.to(torch.int32).contiguous())
+    return _int32(tables), _int32(seq_lens), None if n_new is None else _int32(n_new)
 
 
 class Rotary:
@@ -425,6 +465,7 @@ class Rotary:
         self.table = table
         self.desc = _lib.RotaryDesc(2 * pairs, int(interleaved), n_axes, table.shape[0], table.data_ptr(),
                                     (ctypes.c_uint8 * _lib.MAX_PAIRS)(*axis))
+        self._ref = ctypes.byref(self.desc)
 
     @staticmethod
     def make_table(inv_freq: torch.Tensor, max_positions: int, device="cuda") -> torch.Tensor:
@@ -610,6 +651,8 @@ class ExtendPlan:
         self.c = _lib.ExtendPlan()
         check(lib().q4kv_extend_plan_make(batch, max_new, n_q_heads, n_kv_heads, head_dim, max_blocks_per_seq, window,
                                           n_splits, num_sms, ctypes.byref(self.c)), "q4kv_extend_plan_make")
+        self._ref = ctypes.byref(self.c)
+        self._shape = (batch, max_new, n_q_heads, max_blocks_per_seq, window)
 
     def __getattr__(self, name):
         return getattr(self.__dict__["c"], name)
@@ -629,28 +672,29 @@ def extend_attention(pool: Q4KVPool, q: torch.Tensor, block_tables: torch.Tensor
     seq_lens holds the lengths before the new tokens: token i < n_new[b] (all T
     when n_new is None) sees positions t <= seq_lens[b] + i and, with window >
     0, t > seq_lens[b] + i - window.  Rows at or past n_new[b] are 0."""
-    dev = _require_cuda(pool.mask, q, block_tables, seq_lens, n_new, workspace, out)
+    dev = _same_device(pool.mask, q, block_tables, seq_lens, n_new, workspace, out)
     _check_chunk(q, "q")
     B, T, hq, d = q.shape
     tab, lens, nn = _sequences(B, block_tables, seq_lens, n_new)
-    with torch.cuda.device(dev):
-        if plan is None:
+    if plan is None:
+        with torch.cuda.device(dev):
             plan = ExtendPlan(B, T, hq, pool.n_kv_heads, d, tab.shape[1], window=window)
-        elif (plan.batch, plan.max_new, plan.n_q_heads, plan.max_blocks_per_seq, plan.window) != \
-                (B, T, hq, tab.shape[1], window):
-            raise ValueError("the plan was made for another batch, chunk, head count, table width or window")
-        if workspace is None:
-            workspace = plan.workspace(dev)
-        if out is None:
-            out = torch.empty((B, T, hq, d), dtype=out_dtype, device=dev)
-        elif out.shape != q.shape or out.dtype not in _OUT_DTYPES or out.stride(3) != 1 or out.stride(2) != d:
-            raise ValueError("out must be [B][T][Hq][D] with contiguous rows")
-        qs, os_ = _row_strides(q), _row_strides(out)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        check(lib().q4kv_extend_attention(ctypes.byref(pool.desc), ctypes.byref(plan.c), _ptr(q), _IN_DTYPES[q.dtype],
-                                          qs[0], qs[1], _ptr(tab), _ptr(lens), _ptr(nn), float(softmax_scale),
-                                          _ptr(out), _OUT_DTYPES[out.dtype], os_[0], os_[1], _ptr(workspace),
-                                          ws_bytes, _stream(dev)), "q4kv_extend_attention")
+    elif plan._shape != (B, T, hq, tab.shape[1], window):
+        raise ValueError("the plan was made for another batch, chunk, head count, table width or window")
+    if workspace is None:
+        workspace = plan.workspace(q.device)
+    if out is None:
+        out = torch.empty((B, T, hq, d), dtype=out_dtype, device=q.device)
+        os_ = (T * hq * d, hq * d)
+    elif out.shape != q.shape or out.dtype not in _OUT_DTYPES or out.stride(3) != 1 or out.stride(2) != d:
+        raise ValueError("out must be [B][T][Hq][D] with contiguous rows")
+    else:
+        os_ = _row_strides(out)
+    qs = _row_strides(q)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(dev, "q4kv_extend_attention", pool._ref, plan._ref, q.data_ptr(), _IN_DTYPES[q.dtype], qs[0], qs[1],
+          tab.data_ptr(), lens.data_ptr(), _addr(nn), softmax_scale, out.data_ptr(), _OUT_DTYPES[out.dtype], os_[0], os_[1],
+          _addr(workspace), ws_bytes)
     return out
 
 
