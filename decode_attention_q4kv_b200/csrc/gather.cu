@@ -11,6 +11,12 @@
 // through fp16 (0x64xx is 1024 + xx: a mask, an or and a subtraction, exact);
 // integer conversions would go through the special-function unit at a quarter
 // of the rate.
+//
+// Bound by memory: 10 x 32768 tokens of 8 heads of 128, a quarter of the blocks
+// 8-bit, to fp16 with the keys un-rotated take 322 us, 5.6 TB/s of the 1.8 GB that
+// have to move (0.87 of the copy bandwidth).  With one head per look-up and
+// integer conversions it was 483 us; without the codes of the next head on
+// their way 404 us; at 3 blocks per SM instead of 4, 348 us.
 #include "encode.cuh"
 #include "extend_internal.cuh"
 
@@ -95,70 +101,85 @@ __device__ __forceinline__ uint32_t pack_out<__nv_bfloat16>(float lo, float hi) 
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Outputs are not read again here: streaming stores leave the L2 to the codes.
 template <typename OutT>
 __device__ __forceinline__ void store_pairs(OutT* dst, const float2 (&x)[8]) {
   uint4* d = reinterpret_cast<uint4*>(dst);
-  __stcs(d, make_uint4(pack_out<OutT>(x[0].x, x[1].x), pack_out<OutT>(x[2].x, x[3].x), pack_out<OutT>(x[4].x, x[5].x),
-                       pack_out<OutT>(x[6].x, x[7].x)));
-  __stcs(d + 1, make_uint4(pack_out<OutT>(x[0].y, x[1].y), pack_out<OutT>(x[2].y, x[3].y), pack_out<OutT>(x[4].y, x[5].y),
-                           pack_out<OutT>(x[6].y, x[7].y)));
+  d[0] = make_uint4(pack_out<OutT>(x[0].x, x[1].x), pack_out<OutT>(x[2].x, x[3].x), pack_out<OutT>(x[4].x, x[5].x),
+                    pack_out<OutT>(x[6].x, x[7].x));
+  d[1] = make_uint4(pack_out<OutT>(x[0].y, x[1].y), pack_out<OutT>(x[2].y, x[3].y), pack_out<OutT>(x[4].y, x[5].y),
+                    pack_out<OutT>(x[6].y, x[7].y));
 }
 template <>
 __device__ __forceinline__ void store_pairs<float>(float* dst, const float2 (&x)[8]) {
   float4* d = reinterpret_cast<float4*>(dst);
-  __stcs(d, make_float4(x[0].x, x[1].x, x[2].x, x[3].x));
-  __stcs(d + 1, make_float4(x[4].x, x[5].x, x[6].x, x[7].x));
-  __stcs(d + 2, make_float4(x[0].y, x[1].y, x[2].y, x[3].y));
-  __stcs(d + 3, make_float4(x[4].y, x[5].y, x[6].y, x[7].y));
+  d[0] = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
+  d[1] = make_float4(x[4].x, x[5].x, x[6].x, x[7].x);
+  d[2] = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
+  d[3] = make_float4(x[4].y, x[5].y, x[6].y, x[7].y);
 }
 
-// One head of the lane's row: decode, un-rotate, store.
+// Heads h0 .. h1 - 1 of the lane's row: decode, un-rotate, store.  The codes of
+// the next head are on their way while one is worked on.
 template <int D, typename OutT, int BITS, bool FP8>
-__device__ __forceinline__ void one_head(const PoolView& pool, int64_t row, int j, bool ok, bool masked, bool turn, bool write,
-                                         OutT* kd, OutT* vd) {
+__device__ __forceinline__ void heads(const PoolView& pool, int64_t phys, int slot, int j, int h0, int h1, bool ok, bool masked,
+                                      bool turn, bool write, OutT* kd, OutT* vd) {
   constexpr int NG = D / kGroup;
+  constexpr int64_t kHeadCodes = static_cast<int64_t>(kBlockTokens) * (D / 8 * BITS), kHeadParams = kBlockTokens * NG;
+  const int64_t row = (phys * pool.n_kv_heads + h0) * kBlockTokens + slot;
   const uint8_t* kc = (BITS == 4 ? pool.k_codes4 : BITS == 8 ? pool.k_codes8 : pool.k_codes2) + row * (D / 8 * BITS);
   const uint8_t* vc = (BITS == 4 ? pool.v_codes4 : BITS == 8 ? pool.v_codes8 : pool.v_codes2) + row * (D / 8 * BITS);
   const __half2* kp = (BITS == 4 ? pool.k_params4 : BITS == 8 ? pool.k_params8 : pool.k_params2) + row * NG + (j >> 2);
   const __half2* vp = (BITS == 4 ? pool.v_params4 : BITS == 8 ? pool.v_params8 : pool.v_params2) + row * NG + (j >> 2);
-  float2 x[8], y[8];
-#pragma unroll
-  for (int p = 0; p < 8; ++p) x[p] = y[p] = make_float2(0.0f, 0.0f);
-  if (ok) {
-    const Codes<BITS> ck = load_codes<BITS>(kc, j), cv = load_codes<BITS>(vc, j);
-    if (FP8) {
-      fp8_values(*reinterpret_cast<const Codes<8>*>(&ck), x);
-      fp8_values(*reinterpret_cast<const Codes<8>*>(&cv), y);
-    } else {
-      const __half2 sk = __ldg(kp), sv = __ldg(vp);
-      to_values<BITS>(ck, sk, x);
-      to_values<BITS>(cv, sv, y);
+  Codes<BITS> nk = {}, nv = {};
+  __half2 nsk = {}, nsv = {};
+  auto fetch = [&]() {
+    nk = load_codes<BITS>(kc, j);
+    nv = load_codes<BITS>(vc, j);
+    kc += kHeadCodes;
+    vc += kHeadCodes;
+    if (!FP8) {
+      nsk = __ldg(kp);
+      nsv = __ldg(vp);
+      kp += kHeadParams;
+      vp += kHeadParams;
     }
-  }
-  __syncwarp();
-  if (turn) {
-    rotate_pairs<D>(x, j);
-    if (kRotScale<D> != 1.0f) {
+  };
+  if (ok) fetch();
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const Codes<BITS> ck = nk, cv = nv;
+    const __half2 sk = nsk, sv = nsv;
+    if (ok && h + 1 < h1) fetch();
+    float2 x[8];
+    if (FP8) fp8_values(*reinterpret_cast<const Codes<8>*>(&ck), x);
+    else to_values<BITS>(ck, sk, x);
+    if (turn) {
+      rotate_pairs<D>(x, j);
+      if (kRotScale<D> != 1.0f) {
 #pragma unroll
-      for (int p = 0; p < 8; ++p) x[p] = make_float2(x[p].x * kRotScale<D>, x[p].y * kRotScale<D>);
+        for (int p = 0; p < 8; ++p) x[p] = make_float2(x[p].x * kRotScale<D>, x[p].y * kRotScale<D>);
+      }
     }
-  }
-  if (masked) {
+    if (masked || !ok) {
+      const float s = masked ? Q4KV_SENTINEL_LOGIT : 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      x[p] = make_float2(Q4KV_SENTINEL_LOGIT, Q4KV_SENTINEL_LOGIT);
-      y[p] = make_float2(0.0f, 0.0f);
+      for (int p = 0; p < 8; ++p) x[p] = make_float2(s, s);
     }
-  }
-  if (write) {
-    store_pairs<OutT>(kd, x);
-    store_pairs<OutT>(vd, y);
+    if (write) store_pairs<OutT>(kd, x);
+    if (FP8) fp8_values(*reinterpret_cast<const Codes<8>*>(&cv), x);
+    else to_values<BITS>(cv, sv, x);
+    if (masked || !ok) {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) x[p] = make_float2(0.0f, 0.0f);
+    }
+    if (write) store_pairs<OutT>(vd, x);
+    kd += D;
+    vd += D;
   }
 }
 
 template <int D, typename OutT>
-__global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ GatherArgs a, int64_t n_items, int per) {
+__global__ void __launch_bounds__(256, 4) gather_kernel(const __grid_constant__ GatherArgs a, int64_t n_items, int per) {
   using S = Shape<D>;
   griddep_wait();
   griddep_launch_dependents();
@@ -209,22 +230,19 @@ __global__ void __launch_bounds__(256) gather_kernel(const __grid_constant__ Gat
   const int h1 = min(hkv, (part + 1) * per);
   // the widths of a warp's rows differ only where a block ends among them
   const bool all4 = __all_sync(0xffffffffu, bits == 4), all8 = __all_sync(0xffffffffu, bits == 8);
-#pragma unroll 1
-  for (int h = part * per; h < h1; ++h) {
-    const int64_t row = (phys * hkv + h) * kBlockTokens + slot;
-    OutT* kd = static_cast<OutT*>(a.k_out) + at + static_cast<int64_t>(h) * D;
-    OutT* vd = static_cast<OutT*>(a.v_out) + at + static_cast<int64_t>(h) * D;
-    if (pool.fp8) {
-      one_head<D, OutT, 8, true>(pool, row, j, ok, masked, false, inside, kd, vd);
-    } else if (all4) {
-      one_head<D, OutT, 4, false>(pool, row, j, ok, masked, turn, inside, kd, vd);
-    } else if (all8) {
-      one_head<D, OutT, 8, false>(pool, row, j, ok, masked, turn, inside, kd, vd);
-    } else {                                     // every lane takes part in each (the rotation shuffles)
-      one_head<D, OutT, 4, false>(pool, row, j, ok && bits == 4, masked, turn, inside && bits == 4, kd, vd);
-      one_head<D, OutT, 8, false>(pool, row, j, ok && bits == 8, masked, turn, inside && bits == 8, kd, vd);
-      one_head<D, OutT, 2, false>(pool, row, j, ok && bits == 2, masked, turn, inside && bits == 2, kd, vd);
-    }
+  const int h0 = part * per;
+  OutT* kd = static_cast<OutT*>(a.k_out) + at + static_cast<int64_t>(h0) * D;
+  OutT* vd = static_cast<OutT*>(a.v_out) + at + static_cast<int64_t>(h0) * D;
+  if (pool.fp8) {
+    heads<D, OutT, 8, true>(pool, phys, slot, j, h0, h1, ok, masked, false, inside, kd, vd);
+  } else if (all4) {
+    heads<D, OutT, 4, false>(pool, phys, slot, j, h0, h1, ok, masked, turn, inside, kd, vd);
+  } else if (all8) {
+    heads<D, OutT, 8, false>(pool, phys, slot, j, h0, h1, ok, masked, turn, inside, kd, vd);
+  } else {                                       // every lane takes part in each (the rotation shuffles)
+    heads<D, OutT, 4, false>(pool, phys, slot, j, h0, h1, ok && bits == 4, masked, turn, inside && bits == 4, kd, vd);
+    heads<D, OutT, 8, false>(pool, phys, slot, j, h0, h1, ok && bits == 8, masked, turn, inside && bits == 8, kd, vd);
+    heads<D, OutT, 2, false>(pool, phys, slot, j, h0, h1, ok && bits == 2, masked, turn, inside && bits == 2, kd, vd);
   }
 }
 

@@ -161,26 +161,31 @@ __global__ void __launch_bounds__(256) append_rotary_kernel(const __grid_constan
       }
     }
 
-    const int g_end = min(groups, (part + 1) * per);
-    for (int gi = part * per; gi < g_end; ++gi) {
-      if (gi >= kv_groups) {                     // queries
-        const int h = (gi - kv_groups) * S::VPW + r;
-        const bool valid = h < hq;
-        const int hs = valid ? h : hq - 1;       // lanes past the last head read a real row, store nothing
-        const int64_t at = static_cast<int64_t>(hs) * D + j * kEPL;
-        uint32_t w[8] = {};
-        if (ok) {
-          load_words(static_cast<const InT*>(a.q) + b * a.q_seq_stride + i * a.q_token_stride + at, w);
-          turn_words<InT, INTER>(w, t);
-        }
-        if (valid) {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<InT*>(a.q_out) + b * a.o_seq_stride + i * a.o_token_stride + at);
+    const int g0 = part * per, g1 = min(groups, (part + 1) * per);
+    // queries: a group's row is on its way while the one before is turned
+    const int q0 = max(g0, kv_groups);
+    if (q0 < g1) {
+      const InT* src = static_cast<const InT*>(a.q) + b * a.q_seq_stride + i * a.q_token_stride + j * kEPL;
+      InT* dst = static_cast<InT*>(a.q_out) + b * a.o_seq_stride + i * a.o_token_stride + j * kEPL;
+      // lanes past the last head read a real row, store nothing
+      auto head = [&](int g) { return min((g - kv_groups) * S::VPW + r, hq - 1); };
+      uint32_t w[8] = {}, next[8] = {};
+      if (ok) load_words(src + static_cast<int64_t>(head(q0)) * D, next);
+#pragma unroll 1
+      for (int gi = q0; gi < g1; ++gi) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = next[e];
+        if (ok && gi + 1 < g1) load_words(src + static_cast<int64_t>(head(gi + 1)) * D, next);
+        if (ok) turn_words<InT, INTER>(w, t);
+        if ((gi - kv_groups) * S::VPW + r < hq) {
+          uint4* o = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(head(gi)) * D);
           o[0] = make_uint4(w[0], w[1], w[2], w[3]);
           o[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
-        continue;
       }
-      if (!ok) continue;
+    }
+    if (!ok) continue;
+    for (int gi = g0; gi < min(g1, kv_groups); ++gi) {
       const int slot = static_cast<int>(p % kBlockTokens);
       const int h = gi * S::VPW + r;
       const bool valid = h < hkv;
