@@ -534,3 +534,16 @@ q4kv_status q4kv_read_device_error(const q4kv_pool* pool, uint32_t* bits, int32_
 }
 
 }  // extern "C"
+
+// Single-token attention over seq_lens[b] + 1 tokens: the one-token chunk.
+q4kv_status q4kv::one_token_attention(const q4kv_pool* pool, const q4kv_decode_plan* plan, const void* q, int32_t q_dtype,
+                           const int32_t* block_tables, const int32_t* seq_lens, float softmax_scale, void* out,
+                           int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  DecodeArgs a;
+  int empty = 1;
+  const q4kv_status st = prepare_decode(pool, plan, q, q_dtype, block_tables, seq_lens, softmax_scale, out,
+                                        out_dtype, workspace, workspace_bytes, &a, &empty);
+  if (st != Q4KV_OK || empty) return st;
+  a.add_const = 1;
+  return from_cuda(launch_decode(a, as_stream(stream)));
+}

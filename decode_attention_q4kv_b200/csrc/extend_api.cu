@@ -113,6 +113,12 @@ q4kv_status q4kv_gather_tokens(const q4kv_pool* pool, const int32_t* tables, int
   return from_cuda(launch_gather(a, as_stream(stream)));
 }
 
+// One new token per sequence is what the decode kernel does; it reads the codes
+// without turning them into fp16 tiles.
+static bool one_token(int32_t max_new, int32_t window, int g, int32_t head_dim) {
+  return max_new == 1 && window == 0 && g <= 8 && g * head_dim <= 1024;
+}
+
 // decode_splits < 0 lets the decode planner choose from num_sms.
 static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                              int32_t max_blocks, int32_t window, int32_t n_splits, int32_t decode_splits,
@@ -179,6 +185,16 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
     const size_t rows = static_cast<size_t>(batch) * max_new * n_q_heads * partials;
     plan->workspace_bytes = round_up(rows * head_dim * sizeof(float), 256) + round_up(rows * sizeof(float2), 256);
   }
+  if (one_token(max_new, window, g, head_dim)) {
+    q4kv_decode_plan d;
+    const q4kv_status st = q4kv_decode_plan_make(batch, n_q_heads, n_kv_heads, head_dim, max_blocks,
+                                                 decode_splits < 0 ? 0 : decode_splits, num_sms, &d);
+    if (st != Q4KV_OK) return st;
+    plan->decode_splits = d.n_splits;
+    plan->workspace_bytes = max(plan->workspace_bytes, d.workspace_bytes);
+  } else if (decode_splits > 0) {
+    return Q4KV_ERR_INVALID_ARG;
+  }
   return Q4KV_OK;
 }
 
@@ -204,7 +220,7 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
                  plan->max_blocks_per_seq, plan->window, plan->n_splits, plan->decode_splits, 1, &ref);
   if (st != Q4KV_OK) return st;
   if (plan->head_dim != pool->head_dim || plan->n_kv_heads != pool->n_kv_heads || ref.n_splits != plan->n_splits ||
-      ref.workspace_bytes != plan->workspace_bytes)
+      ref.decode_splits != plan->decode_splits || ref.workspace_bytes != plan->workspace_bytes)
     return Q4KV_ERR_INVALID_ARG;
   if ((q_dtype != Q4KV_F16 && q_dtype != Q4KV_BF16) ||
       (out_dtype != Q4KV_F32 && out_dtype != Q4KV_F16 && out_dtype != Q4KV_BF16) || !isfinite(softmax_scale))
@@ -221,6 +237,17 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   if (plan->workspace_bytes > 0 &&
       (workspace == nullptr || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256)))
     return Q4KV_ERR_WORKSPACE;
+  // (the decode kernel's rows of codes are numbered in 32 bits)
+  const int64_t widest = max(pool->n_q4_blocks, max(pool->n_q8_blocks, pool->n_q2_blocks));
+  if (plan->decode_splits > 0 && n_new == nullptr && (plan->batch == 1 || (q_seq_stride == row && out_seq_stride == row)) &&
+      widest * pool->n_kv_heads * kBlockTokens < (int64_t{1} << 31)) {
+    q4kv_decode_plan d;
+    st = q4kv_decode_plan_make(plan->batch, plan->n_q_heads, plan->n_kv_heads, plan->head_dim, plan->max_blocks_per_seq,
+                               plan->decode_splits, 1, &d);
+    if (st != Q4KV_OK) return st;
+    return one_token_attention(pool, &d, q, q_dtype, block_tables, seq_lens, softmax_scale, out, out_dtype, workspace,
+                               workspace_bytes, stream);
+  }
   ExtendArgs a;
   a.pool = view_of(*pool);
   a.plan = *plan;

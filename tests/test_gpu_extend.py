@@ -238,14 +238,26 @@ def test_bad_lengths_and_blocks_zero_the_rows_and_raise(T):
     _attend_close(out[2], want[2], bound[2])
 
 
-def test_one_token_equals_decode_and_general_path():
-    c = Case([900, 17, 256], 1, 8, 2, 128, "fp16", seed=12)
-    a = c.run()
+@pytest.mark.parametrize("widths,fp8,d", [((4,), False, 128), ((4, 8, 2), False, 256), ((4,), True, 128)])
+def test_one_token_equals_decode_and_general_path(widths, fp8, d):
+    # without counts one token takes the decode kernel, with counts the chunk kernel
+    c = Case([900, 17, 256], 1, 8, 2, d, "fp16", seed=12, widths=widths, fp8=fp8)
     lens = c.dev([n + 1 for n in c.lens])
     b = q4.decode_attention(c.pool, c.q.to(cuda())[:, 0].contiguous(), c.dev(c.tables), lens, out_dtype=torch.float32)
     want, bound = c.want()
+    a = c.run()
+    assert torch.equal(a[:, 0], b)
     _attend_close(a, want, bound)
-    assert float((a[:, 0] - b).abs().max()) < 2e-3
+    c.n_new = [1, 1, 1]
+    _attend_close(c.run(), want, bound)
+    c.n_new = [1, 0, 1]
+    out = c.run()
+    assert torch.count_nonzero(out[1]) == 0
+    _attend_close(out[0::2], want[0::2], bound[0::2])
+    assert c.pool.read_device_error() == 0
+    c.n_new, c.lens = None, [900, -1, 256]
+    out = c.run()
+    assert torch.count_nonzero(out[1]) == 0 and c.pool.read_device_error() & _lib.DEVERR_SEQ_LEN
 
 
 def test_capture_replay_streams_and_repeats():
