@@ -230,17 +230,17 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
       !rows_ok(out, out_seq_stride, out_token_stride, row, out_dtype == Q4KV_F32 ? 4 : 2))
     return Q4KV_ERR_INVALID_ARG;
-  if (block_tables == nullptr || !aligned(block_tables, 16) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
+  if (block_tables == nullptr || !aligned(block_tables, 4) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
       (n_new != nullptr && !aligned(n_new, 4)))
     return Q4KV_ERR_INVALID_ARG;
   if (pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks == 0) return Q4KV_ERR_INVALID_ARG;
   if (plan->workspace_bytes > 0 &&
       (workspace == nullptr || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256)))
     return Q4KV_ERR_WORKSPACE;
-  // (the decode kernel's rows of codes are numbered in 32 bits)
+  // (the decode kernel wants aligned tables and numbers rows of codes in 32 bits)
   const int64_t widest = max(pool->n_q4_blocks, max(pool->n_q8_blocks, pool->n_q2_blocks));
   if (plan->decode_splits > 0 && n_new == nullptr && (plan->batch == 1 || (q_seq_stride == row && out_seq_stride == row)) &&
-      widest * pool->n_kv_heads * kBlockTokens < (int64_t{1} << 31)) {
+      aligned(block_tables, 16) && widest * pool->n_kv_heads * kBlockTokens < (int64_t{1} << 31)) {
     q4kv_decode_plan d;
     st = q4kv_decode_plan_make(plan->batch, plan->n_q_heads, plan->n_kv_heads, plan->head_dim, plan->max_blocks_per_seq,
                                plan->decode_splits, 1, &d);

@@ -131,7 +131,8 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  *   n_new        device int32 [batch], 0 <= n_new[b] <= max_new; NULL =
  *                max_new for every sequence
  *   block_tables device int32 [batch][max_blocks_per_seq]
- *   out          as q, of out_dtype (F32, F16 or BF16), its own strides
+ *   out          as q, of out_dtype (F32, F16 or BF16), its own strides; must
+ *                not overlap q
  *   softmax_scale <= 0 selects 1/sqrt(D)
  *   workspace    as for q4kv_decode_attention
  * Token i of sequence b sees the positions t <= seq_lens[b] + i and, with
@@ -140,6 +141,8 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  * slots only returns 0.  Rows at or past n_new[b] are written as 0.  Keys and
  * values are rounded to fp16 (relative 2^-11) for the tensor cores, so
  * dequantised values must lie inside fp16's range.
+ * One new token per sequence (max_new == 1, no window, n_new NULL, rows next to
+ * each other) takes the kernel of q4kv_decode_attention, with its accuracy.
  * A sequence longer than its table raises Q4KV_DEVERR_SEQ_LEN, a block id out
  * of range Q4KV_DEVERR_BLOCK_ID; the affected rows are written as 0.
  */

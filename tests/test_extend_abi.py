@@ -69,7 +69,7 @@ def test_attention_refusals():
     assert _attend(qdt=2) == BAD and _attend(odt=3) == BAD and _attend(scale=float("nan")) == BAD
     assert _attend(q=None) == BAD and _attend(q=FAKE + 8) == BAD and _attend(out=None) == BAD and _attend(out=FAKE + 2) == BAD
     assert _attend(qs=(7 * 4096, 4095)) == BAD and _attend(qs=(7 * 4096 + 4, 4096)) == BAD and _attend(os_=(7 * 4096, 1024)) == BAD
-    assert _attend(tab=None) == BAD and _attend(tab=FAKE + 4) == BAD and _attend(lens=None) == BAD and _attend(nn=FAKE + 2) == BAD
+    assert _attend(tab=None) == BAD and _attend(tab=FAKE + 2) == BAD and _attend(lens=None) == BAD and _attend(nn=FAKE + 2) == BAD
     assert _attend(pool=_pool(n_q4_blocks=0)) == BAD
     assert _attend(pool=_pool(n_kv_heads=4)) == BAD                # the plan's heads are not the pool's
     st, p = _plan(splits=4)

@@ -284,6 +284,63 @@ def test_capture_replay_streams_and_repeats():
         assert torch.equal(out, first)           # no atomics: bit for bit
 
 
+def test_tables_of_any_alignment_and_two_streams_at_once():
+    # a slice of a wider table starts at any int32; two calls with their own
+    # scratch run beside each other
+    dev = cuda()
+    cases = [Case([500, 900, 33], T, 8, 2, 128, "fp16", seed=T) for T in (1, 20)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args, outs = [], [None, None]
+    for c in cases:
+        mb = c.tables.shape[1]
+        wide = torch.full((3 * mb + 1,), -7, dtype=torch.int32, device=dev)
+        wide[1:] = c.dev(c.tables).flatten()
+        args.append((c.pool, c.q.to(dev), wide[1:].view(3, mb), c.dev(c.lens)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                outs[i] = q4.extend_attention(*args[i], out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, outs):
+        want, bound = c.want()
+        _attend_close(o, want, bound)
+
+
+def test_empty_calls():
+    dev = cuda()
+    c = Case([10], 3, 8, 2, 128, "fp16")
+    out = q4.extend_attention(c.pool, c.q.to(dev)[:, :0], c.dev(c.tables), c.dev(c.lens))
+    assert out.shape == (1, 0, 8, 128)
+    out = q4.extend_attention(c.pool, c.q.to(dev)[:0], c.dev(c.tables)[:0], c.dev(c.lens)[:0])
+    assert out.shape == (0, 3, 8, 128)
+    assert torch.count_nonzero(c.run(out_dtype=torch.float16)) > 0
+
+
+@pytest.mark.parametrize("bad", ["dtype", "heads", "plan", "device", "out", "lens", "counts"])
+def test_attention_arguments_are_checked(bad):
+    dev = cuda()
+    c = Case([10], 3, 8, 2, 128, "fp16")
+    q, tab, lens = c.q.to(dev), c.dev(c.tables), c.dev(c.lens)
+    kw = {}
+    if bad == "dtype":
+        q = q.float()
+    elif bad == "heads":
+        q = torch.zeros(1, 3, 9, 128, dtype=torch.float16, device=dev)
+    elif bad == "plan":
+        kw["plan"] = q4.ExtendPlan(1, 4, 8, 2, 128, tab.shape[1])
+    elif bad == "device":
+        lens = lens.cpu()
+    elif bad == "out":
+        kw["out"] = torch.zeros(1, 3, 8, 64, device=dev)
+    elif bad == "lens":
+        lens = torch.zeros(2, dtype=torch.int32, device=dev)
+    else:
+        kw["n_new"] = torch.zeros(3, dtype=torch.int32, device=dev)
+    with pytest.raises((ValueError, q4.Q4KVError)):
+        q4.extend_attention(c.pool, q, tab, lens, **kw)
+
+
 # -- rotary append -------------------------------------------------------------
 
 def _table(pairs, n, seed=0):
@@ -389,6 +446,54 @@ def test_append_rotary_in_place_and_without_queries():
     assert torch.equal(outs[0][0], outs[1][0])
     for x in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(outs[0][1:], x[1:]))
+
+
+@pytest.mark.parametrize("bad", ["heads", "shape", "positions", "q", "q_out", "axis", "table"])
+def test_append_rotary_arguments_are_checked(bad):
+    dev = cuda()
+    pool = q4.Q4KVPool(2, 128, 2, device=dev)
+    k, v, q = (torch.zeros(1, 2, h, 128, device=dev).half() for h in (2, 2, 4))
+    tab, lens = torch.tensor([[1, 0]], device=dev), torch.tensor([3], device=dev)
+    table = _table(64, 64).to(dev)
+    kw = {"q": q}
+    with pytest.raises((ValueError, q4.Q4KVError)):
+        if bad == "heads":
+            k = v = torch.zeros(1, 2, 3, 128, device=dev).half()
+        elif bad == "shape":
+            v = v[:, :1]
+        elif bad == "positions":
+            kw["positions"] = torch.zeros(2, 1, 2, dtype=torch.int32, device=dev)
+        elif bad == "q":
+            kw["q"] = q.bfloat16()
+        elif bad == "q_out":
+            kw = {"q_out": q}
+        elif bad == "axis":
+            q4.Rotary(table, axis_of_pair=[0] * 63 + [4])
+        else:
+            table = table[:, :24].contiguous()
+        pool.append_rotary(k, v, q4.Rotary(table), tab, lens, **kw)
+
+
+def test_pool_over_the_callers_arrays():
+    dev = cuda()
+    a = q4.Q4KVPool(2, 128, 3, 2, device=dev)
+    k, v = W.random_small(600, 2, 128, "fp16", seed=4)
+    a.quantize(k.to(dev), v.to(dev), torch.tensor([4, 1, 2], dtype=torch.int32, device=dev))
+    names = [f"{x}_{p}{w}" for x in "kv" for p in ("codes", "params") for w in "48"]
+    b = q4.Q4KVPool.from_tensors(2, 128, a.mask, **{n: getattr(a, n) for n in names})
+    assert (b.n_q4_blocks, b.n_q8_blocks, b.n_q2_blocks, b.n_blocks) == (3, 2, 0, 5) and b.nbytes() == a.nbytes()
+    ids = torch.tensor([4, 1, 2], dtype=torch.int32, device=dev)
+    assert all(torch.equal(x, y) for x, y in zip(a.dequantize(ids), b.dequantize(ids)))
+    b.append(k[:1, None].to(dev), v[:1, None].to(dev), ids[1:2, None].contiguous(), torch.zeros(1, dtype=torch.int32, device=dev))
+    assert torch.equal(a.k_codes4, b.k_codes4) and a.k_codes4.data_ptr() == b.k_codes4.data_ptr()
+    good = {n: getattr(a, n) for n in names}
+    for n, t in (("k_codes4", a.k_codes4[:, :, :, :32]), ("v_params8", a.v_params8.float()), ("v_codes8", a.v_codes8[:1])):
+        with pytest.raises(ValueError):
+            q4.Q4KVPool.from_tensors(2, 128, a.mask, **{**good, n: t})
+    with pytest.raises(ValueError):
+        q4.Q4KVPool.from_tensors(2, 128, a.mask[:4], **good)
+    with pytest.raises(ValueError):
+        q4.Q4KVPool.from_tensors(2, 128, a.mask, k_codes16=a.k_codes8, **good)
 
 
 def test_append_rotary_faults_skip_the_token():
