@@ -830,20 +830,31 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
     for (int st = 1; st < 32; st <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, st));
     poison = __any_sync(0xffffffffu, poison);
     if (!poison && M != -INFINITY) {
-      for (int p = 0; p < partials; ++p) {
-        const float2 v = a.ws_ml[p * rows + row];
-        if (v.x == -INFINITY) continue;                     // saw no keys; its accumulator may not be written
-        const float f = exp2f(v.x - M);
-        L = fmaf(v.y, f, L);
-        const float* o = a.ws_o + (p * rows + row) * D + lane * E;
+      // four partial results at a time, their loads together
+      for (int p0 = 0; p0 < partials; p0 += 4) {
+        float2 v[4];
+        float4 x[4][E / 4];
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(o + e);
-          acc[e] = fmaf(x.x, f, acc[e]);
-          acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
-          acc[e + 2] = fmaf(x.z, f, acc[e + 2]);
-          acc[e + 3] = fmaf(x.w, f, acc[e + 3]);
-        }
+        for (int q = 0; q < 4; ++q)
+          if (p0 + q < partials) {
+            const int64_t part = (p0 + q) * rows + row;
+            v[q] = a.ws_ml[part];
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) x[q][e] = *reinterpret_cast<const float4*>(a.ws_o + part * D + lane * E + 4 * e);
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (p0 + q < partials && v[q].x != -INFINITY) {   // (one that saw no keys has written no accumulator)
+            const float f = exp2f(v[q].x - M);
+            L = fmaf(v[q].y, f, L);
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e) {
+              acc[4 * e] = fmaf(x[q][e].x, f, acc[4 * e]);
+              acc[4 * e + 1] = fmaf(x[q][e].y, f, acc[4 * e + 1]);
+              acc[4 * e + 2] = fmaf(x[q][e].z, f, acc[4 * e + 2]);
+              acc[4 * e + 3] = fmaf(x[q][e].w, f, acc[4 * e + 3]);
+            }
+          }
       }
     }
   }

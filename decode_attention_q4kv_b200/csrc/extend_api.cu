@@ -147,12 +147,16 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
   const int64_t steps = (ctx + step - 1) / step;
   int64_t s = n_splits;
   if (s == 0) {
-    // Time in SM cycles: waves of CTAs (one per SM), each with its key tiles and
+    // Time in SM cycles: CTAs (one per SM at a time), each with its key tiles and
     // what starting and ending it costs, and the partial results written and
     // read again.  The figures are fitted to times measured with forced split
     // counts: 4200 cycles a step of 128 tokens x 256 rows, 5000 of 256 x 128,
-    // 2700 of 64 x 128 (heads of 256), 27000 a CTA, 3300 bytes a cycle.
-    const double step_cycles = head_dim == 256 ? 2700.0 : sh.rows == 256 ? 4200.0 : 5000.0;
+    // 2400 of 64 x 128 (heads of 256), 27000 a CTA, 3300 bytes a cycle.
+    // Sequences of one length run in waves; of several, a CTA that ends early
+    // makes room for the next (three quarters of the work, and half of the last
+    // CTA's as a tail).  Which it will be is not known here, so a batch is
+    // planned for the mean of both.
+    const double step_cycles = head_dim == 256 ? 2400.0 : sh.rows == 256 ? 4200.0 : 5000.0;
     const double partial_cycles = static_cast<double>(batch) * max_new * n_q_heads * head_dim * 8.0 / 3300.0 * sh.streams;
     const int64_t items = max(int64_t{1}, static_cast<int64_t>(batch) * n_kv_heads * ((group_rows + sh.rows - 1) / sh.rows));
     double best = 1e300;
@@ -160,8 +164,13 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
     for (int64_t cand = 1; cand <= min(steps, int64_t{4} * num_sms); ++cand) {
       const int64_t per = (steps + cand - 1) / cand;
       if ((steps + per - 1) / per != cand) continue;
-      const double cost = static_cast<double>((items * cand + num_sms - 1) / num_sms) * (per * step_cycles + 27000.0) +
-                          (cand * sh.streams > 1 ? cand * partial_cycles + 6000.0 : 0.0);
+      const double one = per * step_cycles + 27000.0;
+      double cost = static_cast<double>((items * cand + num_sms - 1) / num_sms) * one;
+      if (batch > 1) {
+        const double part = static_cast<double>(items * cand) / num_sms * (0.75 * per * step_cycles + 27000.0) + 0.5 * one;
+        cost = 0.5 * (cost + max(part, one));
+      }
+      if (cand * sh.streams > 1) cost += cand * partial_cycles + 6000.0;
       if (cost < best - 1e-9) {
         best = cost;
         s = cand;
