@@ -82,13 +82,22 @@ def _int32(t: torch.Tensor) -> torch.Tensor:
     return t if t.dtype is torch.int32 and t.is_contiguous() else t.to(torch.int32).contiguous()
 
 
+def _public_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# The handle alone; building a Stream object for it takes longer than a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+
+
 def _call(dev: int, name: str, *args) -> None:
     """One library call on a device's current stream (its last argument)."""
+    fn = getattr(lib(), name)
     if torch.cuda.current_device() == dev:
-        status = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+            status = fn(*args, _raw_stream(dev))
     if status:
         check(status, name)
 

@@ -124,6 +124,8 @@ def header_functions(header: str = HEADER):
 def lib() -> ctypes.CDLL:
     """The loaded library, building it first when missing or older than its sources."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
