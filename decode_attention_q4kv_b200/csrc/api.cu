@@ -4,7 +4,7 @@
 #include <math.h>
 #include <string.h>
 
-#include "extend_internal.cuh"
+#include "q4kv_internal.cuh"
 
 using namespace q4kv;
 
@@ -12,9 +12,7 @@ namespace {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-}  // namespace
-
-q4kv_status q4kv::check_pool(const q4kv_pool* p) {
+q4kv_status check_pool(const q4kv_pool* p) {
   if (p == nullptr) return Q4KV_ERR_INVALID_ARG;
   if ((p->value_format != Q4KV_FORMAT_INT && p->value_format != Q4KV_FORMAT_FP8) || p->n_kv_heads < 1 ||
       p->n_q4_blocks < 0 || p->n_q8_blocks < 0 || p->n_q2_blocks < 0 || p->reserved != 0 ||
@@ -46,8 +44,6 @@ q4kv_status q4kv::check_pool(const q4kv_pool* p) {
   if (p->error_word != nullptr && !aligned(p->error_word, 4)) return Q4KV_ERR_INVALID_ARG;
   return Q4KV_OK;
 }
-
-namespace {
 
 q4kv_status check_input(const void* x, int32_t dtype, int64_t n_tokens, int64_t stride,
                         int32_t hkv, int32_t d) {
@@ -83,27 +79,6 @@ inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
-
-// Arguments of an append; *rows = 0 when it writes nothing.
-q4kv_status q4kv::check_append(const q4kv_pool* pool, const void* k, const void* v, int32_t in_dtype,
-                                int32_t batch, int32_t max_new, const int32_t* n_new, int64_t seq_stride,
-                                int64_t token_stride, const int32_t* tables, int32_t max_blocks,
-                                const int32_t* seq_lens, int64_t* rows) {
-  q4kv_status st = check_pool(pool);
-  if (st != Q4KV_OK) return st;
-  if (batch < 0 || max_new < 0 || seq_stride < 0) return Q4KV_ERR_INVALID_ARG;
-  *rows = batch > 0 && max_new > 0 ? 1 : 0;
-  st = check_input(k, in_dtype, *rows, token_stride, pool->n_kv_heads, pool->head_dim);
-  if (st != Q4KV_OK) return st;
-  st = check_input(v, in_dtype, *rows, token_stride, pool->n_kv_heads, pool->head_dim);
-  if (st != Q4KV_OK) return st;
-  if ((seq_stride * 2) % 16 != 0) return Q4KV_ERR_INVALID_ARG;
-  if (*rows == 0) return Q4KV_OK;
-  if (tables == nullptr || !aligned(tables, 4) || max_blocks < 1 || seq_lens == nullptr ||
-      !aligned(seq_lens, 4) || (n_new != nullptr && !aligned(n_new, 4)))
-    return Q4KV_ERR_INVALID_ARG;
-  return Q4KV_OK;
-}
 
 extern "C" {
 
@@ -146,6 +121,27 @@ q4kv_status q4kv_quantize_blocks(const q4kv_pool* pool, const void* k, const voi
   if (block_ids == nullptr || !aligned(block_ids, 4)) return Q4KV_ERR_INVALID_ARG;
   return from_cuda(launch_quantize(view_of(*pool), k, v, in_dtype, n_tokens, token_stride,
                                    block_ids, as_stream(stream)));
+}
+
+// Arguments of an append; *rows = 0 when it writes nothing.
+static q4kv_status check_append(const q4kv_pool* pool, const void* k, const void* v, int32_t in_dtype,
+                                int32_t batch, int32_t max_new, const int32_t* n_new, int64_t seq_stride,
+                                int64_t token_stride, const int32_t* tables, int32_t max_blocks,
+                                const int32_t* seq_lens, int64_t* rows) {
+  q4kv_status st = check_pool(pool);
+  if (st != Q4KV_OK) return st;
+  if (batch < 0 || max_new < 0 || seq_stride < 0) return Q4KV_ERR_INVALID_ARG;
+  *rows = batch > 0 && max_new > 0 ? 1 : 0;
+  st = check_input(k, in_dtype, *rows, token_stride, pool->n_kv_heads, pool->head_dim);
+  if (st != Q4KV_OK) return st;
+  st = check_input(v, in_dtype, *rows, token_stride, pool->n_kv_heads, pool->head_dim);
+  if (st != Q4KV_OK) return st;
+  if ((seq_stride * 2) % 16 != 0) return Q4KV_ERR_INVALID_ARG;
+  if (*rows == 0) return Q4KV_OK;
+  if (tables == nullptr || !aligned(tables, 4) || max_blocks < 1 || seq_lens == nullptr ||
+      !aligned(seq_lens, 4) || (n_new != nullptr && !aligned(n_new, 4)))
+    return Q4KV_ERR_INVALID_ARG;
+  return Q4KV_OK;
 }
 
 q4kv_status q4kv_append_tokens(const q4kv_pool* pool, const void* k, const void* v,
@@ -534,16 +530,3 @@ q4kv_status q4kv_read_device_error(const q4kv_pool* pool, uint32_t* bits, int32_
 }
 
 }  // extern "C"
-
-// Single-token attention over seq_lens[b] + 1 tokens: the one-token chunk.
-q4kv_status q4kv::one_token_attention(const q4kv_pool* pool, const q4kv_decode_plan* plan, const void* q, int32_t q_dtype,
-                           const int32_t* block_tables, const int32_t* seq_lens, float softmax_scale, void* out,
-                           int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
-  DecodeArgs a;
-  int empty = 1;
-  const q4kv_status st = prepare_decode(pool, plan, q, q_dtype, block_tables, seq_lens, softmax_scale, out,
-                                        out_dtype, workspace, workspace_bytes, &a, &empty);
-  if (st != Q4KV_OK || empty) return st;
-  a.add_const = 1;
-  return from_cuda(launch_decode(a, as_stream(stream)));
-}

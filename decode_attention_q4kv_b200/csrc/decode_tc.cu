@@ -1513,7 +1513,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads + (APP ? 32 : 0), 1)
       bool enc_wait = fused;
       const int seq = seq_next.y, fresh_blk = seq_next.x / kBlockTokens;
       if (item + static_cast<int>(gridDim.x) < n_items) seq_next = seq_of(item + gridDim.x);
-      const bool bad_seq = seq_next.x < 0 || seq < 0 || seq > mb * kBlockTokens;
+      const bool bad_seq = seq < 0 || seq > mb * kBlockTokens;
       if (bad_seq && split == 0 && kvh == 0) raise_error(P.error_word, Q4KV_DEVERR_SEQ_LEN);
       const int t0 = split * tps;
       const int t1 = bad_seq ? t0 : min(t0 + tps, seq);

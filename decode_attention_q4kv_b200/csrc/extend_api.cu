@@ -20,6 +20,14 @@ bool rows_ok(const void* p, int64_t seq_stride, int64_t token_stride, int64_t ro
          (token_stride * size) % 16 == 0;
 }
 
+// The checks every call makes of its pool (q4kv_block_image_stride makes them
+// and computes a size on the host).
+q4kv_status check_pool(const q4kv_pool* pool) {
+  size_t stride;
+  return q4kv_block_image_stride(pool, &stride);
+}
+bool has_blocks(const q4kv_pool* pool) { return pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks > 0; }
+
 }  // namespace
 
 extern "C" {
@@ -30,17 +38,23 @@ q4kv_status q4kv_append_rotary(const q4kv_pool* pool, const q4kv_rotary* rotary,
                                int64_t q_seq_stride, int64_t q_token_stride, void* q_out, int64_t q_out_seq_stride,
                                int64_t q_out_token_stride, const int32_t* tables, int32_t max_blocks,
                                const int32_t* seq_lens, const int32_t* positions, void* stream) {
-  int64_t rows = 0;
-  const q4kv_status st = check_append(pool, k, v, in_dtype, batch, max_new, n_new, seq_stride, token_stride, tables,
-                                      max_blocks, seq_lens, &rows);
+  const q4kv_status st = check_pool(pool);
   if (st != Q4KV_OK) return st;
+  if (batch < 0 || max_new < 0 || (in_dtype != Q4KV_F16 && in_dtype != Q4KV_BF16)) return Q4KV_ERR_INVALID_ARG;
+  const bool rows = batch > 0 && max_new > 0;
+  if (rows) {
+    const int64_t row = static_cast<int64_t>(pool->n_kv_heads) * pool->head_dim;
+    if (!rows_ok(k, seq_stride, token_stride, row, 2) || !rows_ok(v, seq_stride, token_stride, row, 2) || !has_blocks(pool) ||
+        tables == nullptr || !aligned(tables, 4) || max_blocks < 1 || seq_lens == nullptr || !aligned(seq_lens, 4) ||
+        (n_new != nullptr && !aligned(n_new, 4)))
+      return Q4KV_ERR_INVALID_ARG;
+  }
   if (rotary == nullptr || (rotary->interleaved != 0 && rotary->interleaved != 1) || rotary->n_axes < 1 ||
       rotary->n_axes > Q4KV_MAX_AXES || rotary->max_positions < 1 || rotary->rot_dim < 32 || rotary->rot_dim % 32 != 0 ||
       rotary->rot_dim > pool->head_dim || rotary->table == nullptr || !aligned(rotary->table, 16))
     return Q4KV_ERR_INVALID_ARG;
   for (int f = 0; f < rotary->rot_dim / 2; ++f)
     if (rotary->axis[f] >= rotary->n_axes) return Q4KV_ERR_INVALID_ARG;
-  if (rows > 0 && pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks == 0) return Q4KV_ERR_INVALID_ARG;
   if (positions != nullptr && !aligned(positions, 4)) return Q4KV_ERR_INVALID_ARG;
   RotaryAppendArgs a;
   a.q = nullptr;
@@ -63,7 +77,7 @@ q4kv_status q4kv_append_rotary(const q4kv_pool* pool, const q4kv_rotary* rotary,
     a.o_seq_stride = q_out_seq_stride;
     a.o_token_stride = q_out_token_stride;
   }
-  if (rows == 0) return Q4KV_OK;
+  if (!rows) return Q4KV_OK;
   a.pool = view_of(*pool);
   a.rot = *rotary;
   a.k = k;
@@ -242,10 +256,11 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   if (block_tables == nullptr || !aligned(block_tables, 4) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
       (n_new != nullptr && !aligned(n_new, 4)))
     return Q4KV_ERR_INVALID_ARG;
-  if (pool->n_q4_blocks + pool->n_q8_blocks + pool->n_q2_blocks == 0) return Q4KV_ERR_INVALID_ARG;
+  if (!has_blocks(pool)) return Q4KV_ERR_INVALID_ARG;
   if (plan->workspace_bytes > 0 &&
       (workspace == nullptr || workspace_bytes < plan->workspace_bytes || !aligned(workspace, 256)))
     return Q4KV_ERR_WORKSPACE;
+  const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(plan->head_dim));
   // (the decode kernel wants aligned tables and numbers rows of codes in 32 bits)
   const int64_t widest = max(pool->n_q4_blocks, max(pool->n_q8_blocks, pool->n_q2_blocks));
   if (plan->decode_splits > 0 && n_new == nullptr && (plan->batch == 1 || (q_seq_stride == row && out_seq_stride == row)) &&
@@ -254,8 +269,23 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
     st = q4kv_decode_plan_make(plan->batch, plan->n_q_heads, plan->n_kv_heads, plan->head_dim, plan->max_blocks_per_seq,
                                plan->decode_splits, 1, &d);
     if (st != Q4KV_OK) return st;
-    return one_token_attention(pool, &d, q, q_dtype, block_tables, seq_lens, softmax_scale, out, out_dtype, workspace,
-                               workspace_bytes, stream);
+    DecodeArgs a = {};
+    a.pool = view_of(*pool);
+    a.plan = d;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.tables = block_tables;
+    a.seq_lens = seq_lens;
+    a.add_const = 1;                       // the sequence with its new token
+    a.scale = scale;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.ws_o = static_cast<float*>(workspace);
+    if (d.workspace_bytes > 0) {
+      const size_t partials = static_cast<size_t>(d.batch) * d.n_q_heads * d.n_splits;
+      a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(partials * d.head_dim * sizeof(float), 256));
+    }
+    return from_cuda(launch_decode(a, as_stream(stream)));
   }
   ExtendArgs a;
   a.pool = view_of(*pool);
@@ -267,7 +297,7 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   a.tables = block_tables;
   a.seq_lens = seq_lens;
   a.n_new = n_new;
-  a.scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(plan->head_dim));
+  a.scale = scale;
   a.out = out;
   a.out_dtype = out_dtype;
   a.o_seq_stride = out_seq_stride;

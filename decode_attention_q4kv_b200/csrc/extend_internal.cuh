@@ -68,15 +68,4 @@ inline ExtendShape extend_shape(int d, int64_t group_rows) {
   return group_rows > 128 ? ExtendShape{256, 128, 1} : ExtendShape{128, 128, 2};
 }
 
-// Single-token attention over seq_lens[b] + 1 tokens by the decode kernel (api.cu).
-q4kv_status one_token_attention(const q4kv_pool* pool, const q4kv_decode_plan* plan, const void* q, int32_t q_dtype,
-                                const int32_t* block_tables, const int32_t* seq_lens, float softmax_scale, void* out,
-                                int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
-
-// Host argument checks shared with api.cu.
-q4kv_status check_pool(const q4kv_pool* p);
-q4kv_status check_append(const q4kv_pool* pool, const void* k, const void* v, int32_t in_dtype, int32_t batch,
-                         int32_t max_new, const int32_t* n_new, int64_t seq_stride, int64_t token_stride,
-                         const int32_t* tables, int32_t max_blocks, const int32_t* seq_lens, int64_t* rows);
-
 }  // namespace q4kv

@@ -142,7 +142,8 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  * values are rounded to fp16 (relative 2^-11) for the tensor cores, so
  * dequantised values must lie inside fp16's range.
  * One new token per sequence (max_new == 1, no window, n_new NULL, rows next to
- * each other) takes the kernel of q4kv_decode_attention, with its accuracy.
+ * each other) takes the kernel of q4kv_decode_attention, with its accuracy;
+ * there a length of -1 is an empty sequence (row 0, no error bit).
  * A sequence longer than its table raises Q4KV_DEVERR_SEQ_LEN, a block id out
  * of range Q4KV_DEVERR_BLOCK_ID; the affected rows are written as 0.
  */

@@ -255,9 +255,10 @@ def test_one_token_equals_decode_and_general_path(widths, fp8, d):
     assert torch.count_nonzero(out[1]) == 0
     _attend_close(out[0::2], want[0::2], bound[0::2])
     assert c.pool.read_device_error() == 0
-    c.n_new, c.lens = None, [900, -1, 256]
-    out = c.run()
-    assert torch.count_nonzero(out[1]) == 0 and c.pool.read_device_error() & _lib.DEVERR_SEQ_LEN
+    for bad in (-2, 5000):
+        c.n_new, c.lens = None, [900, bad, 256]
+        out = c.run()
+        assert torch.count_nonzero(out[1]) == 0 and c.pool.read_device_error() & _lib.DEVERR_SEQ_LEN
 
 
 def test_capture_replay_streams_and_repeats():
