@@ -93,6 +93,7 @@ struct Misc {
   // the keys of tile j + 6 are used up, and the softmax is past tile j.)
   alignas(16) uint32_t gone[8][4];
   int bad[8];
+  int odd_first, odd_last; // tokens of this CTA whose value is not finite lie between these
   float reference[256];    // per row: the reference maximum after the last step that settled
   int8_t exponent[256];    // per row: q was scaled by 2^(6 - exponent)
 };
@@ -188,12 +189,53 @@ __device__ __forceinline__ void codes_fp8(uint32_t w0, uint32_t w1, bool live, u
   }
 }
 
+// Scale and zero of a group whose largest code decodes to a finite fp16 value.
+// A scale rounded up may carry a finite group past fp16 (the error of 15 s is at
+// most half a step of s times 15, and one step less of s takes back twice that);
+// what is still not finite then makes the token odd.
+template <int MAX>
+__device__ __forceinline__ bool finite_group(uint32_t sz) {
+  const __half2 q = u2h(sz);
+  return __hle(__habs(__hfma(__low2half(q), __int2half_rn(MAX), __high2half(q))), __ushort_as_half(0x7BFFu));
+}
+template <int MAX>
+__device__ __forceinline__ bool tame_group(uint32_t& sz) {
+  if (finite_group<MAX>(sz)) return true;
+  if ((sz & 0x7FFFu) != 0) --sz;
+  return finite_group<MAX>(sz);
+}
+// Some byte is an E4M3 NaN.
+__device__ __forceinline__ bool fp8_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+
+// Whether the value of token t, which is not remapped, is finite.
+template <int D>
+__device__ __noinline__ bool odd_token(const PoolView& P, const int32_t* table, int h, int t) {
+  const int blk = __ldg(table + t / kBlockTokens), slot = t % kBlockTokens;
+  if (blk < 0 || blk >= P.n_blocks()) return false;
+  if ((__ldg(P.mask + static_cast<int64_t>(blk) * kMaskWords + slot / 32) >> (slot % 32)) & 1u) return false;
+  const int bits = P.bits_of(blk);
+  const int64_t phys = bits == 4 ? blk : (bits == 8 ? blk - P.n_q4 : blk - P.n_q4 - P.n_q8);
+  const int64_t row = (phys * P.n_kv_heads + h) * kBlockTokens + slot;
+  bool odd = false;
+  if (P.fp8) {
+    for (int i = 0; i < D / 4; ++i) odd |= fp8_nan(__ldg(reinterpret_cast<const uint32_t*>(P.v_codes8 + row * D) + i));
+    return odd;
+  }
+  const __half2* params = (bits == 4 ? P.v_params4 : (bits == 8 ? P.v_params8 : P.v_params2)) + row * (D / kGroup);
+  for (int i = 0; i < D / kGroup; ++i) {
+    uint32_t sz = h2u(__ldg(params + i));
+    odd |= !(bits == 4 ? tame_group<15>(sz) : (bits == 8 ? tame_group<255>(sz) : tame_group<3>(sz)));
+  }
+  return odd;
+}
+
 // The lane's four tokens of a tile, 32 channels each.  The loads come first so
 // that their latencies overlap.  A token that does not count takes scale and
-// zero 0 (whatever its own are), so its values are 0.  BITS 0: E4M3 bytes.
+// zero 0 (whatever its own are), so its values are 0.  With `check` 8-bit codes
+// are looked at for values that are not finite, as below.  BITS 0: E4M3 bytes.
 template <int D, int BITS>
 __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* params, const Lane& ln, uint32_t live,
-                                            uint8_t* dst) {
+                                            uint8_t* dst, bool check, int t0, Misc* ms) {
   constexpr int W = BITS == 0 ? 8 : BITS;              // words of 32 codes
   constexpr int TS = Lane::step(D);
   constexpr int ROW = D / 8 * W;                       // bytes of a token
@@ -217,7 +259,21 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
       }
     }
     if (BITS != 0) sz = *reinterpret_cast<const uint32_t*>(params + ((ln.t + it * TS) * (D / kGroup) + (ln.u >> 1)) * 4);
-    const bool on = (live >> it) & 1u;
+    bool on = (live >> it) & 1u;
+    if ((BITS == 0 || BITS == 8) && check && on) {
+      if (BITS == 0) {
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) odd |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
+        on = (odd & 0x80808080u) == 0;
+      } else {
+        on = tame_group<255>(sz);
+      }
+      if (!on) {
+        atomicMin(&ms->odd_first, t0 + ln.t + it * TS);
+        atomicMax(&ms->odd_last, t0 + ln.t + it * TS);
+      }
+    }
     const __half2 q = u2h(on ? sz : 0u);
     const __half2 s = __low2half2(q), z = __high2half2(q);
 #pragma unroll
@@ -232,6 +288,40 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
           make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+}
+
+// A value that is not finite takes 0 as well: a product with it would reach the
+// rows that do not see its token, too (a weight of 0 times it is NaN).  Its
+// place is noted, and the rows that do see it become NaN at the end.  (A key's
+// logits are replaced where they are not seen, so keys need none of this.)
+//
+// Whether one of the warp's tokens needs it is found out with one look at their
+// scales, two groups a lane.  Scales in shared memory are put right there, 8-bit
+// ones are left to decode_tile.  (Beside every token's decoding the check cost 8
+// to 13 % of whole calls, in a warp of its own, which delays the decoders, 1 to
+// 16 %; here 1 to 7 %.)
+template <int D, int MAX>
+__device__ __noinline__ void mend_groups(uint2* at, uint2 sz, bool live, int t, Misc* ms) {
+  const bool fx = tame_group<MAX>(sz.x), fy = tame_group<MAX>(sz.y);
+  *at = make_uint2(fx ? sz.x : 0u, fy ? sz.y : 0u);
+  if (live && !(fx && fy)) {
+    atomicMin(&ms->odd_first, t);
+    atomicMax(&ms->odd_last, t);
+  }
+}
+template <int D, int MAX>
+__device__ __forceinline__ bool odd_groups(uint8_t* params, const uint8_t* mask, int dw, int lane, int t0, int end, Misc* ms) {
+  const int t = D == 128 ? dw * 8 + (lane & 7) + 32 * (lane >> 3) : dw * 4 + ((lane >> 1) & 3) + 16 * (lane >> 3);
+  uint2* at = reinterpret_cast<uint2*>(params + t * (D / kGroup) * 4) + (D == 128 ? 0 : lane & 1);
+  const uint2 sz = *at;
+  const bool odd = !(finite_group<MAX>(sz.x) && finite_group<MAX>(sz.y));
+  if (!__any_sync(0xffffffffu, odd)) return false;
+  if (MAX != 255) {
+    const int slot = (t0 & 64) * (D / 256) + t;            // within the 128 slots of the mask
+    if (odd) mend_groups<D, MAX>(at, sz, t0 + t < end && !((mask[slot >> 3] >> (slot & 7)) & 1u), t0 + t, ms);
+    __syncwarp();
+  }
+  return true;
 }
 
 // Output columns 8k .. 8k+7 back in channel order.
@@ -289,7 +379,7 @@ __device__ __forceinline__ Item item_of(const ExtendArgs& a) {
   return w;
 }
 
-template <int MODE>
+template <int MODE, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ ExtendArgs a, uint32_t raw_stride,
                                                              int n_raw) {
   using G = Geo<MODE>;
@@ -346,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     mbar_init(&ms->spare, 1);
     for (int i = 0; i < 8; ++i) mbar_init(&ms->turn[i >> 2][i & 3], 1);
     ms->abort = 0;
+    ms->odd_first = 0x7fffffff;
+    ms->odd_last = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(&ms->tmem, 512);
@@ -545,8 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     for (int n = kind; n < 2 * w.n; n += 2) {
       warp_wait(&ms->raw_full[f], lap, ms);
       const int bits = ms->raw_bits[e];
-      const uint8_t* raw = sm + G::kRawAt + e * raw_stride;
-      const uint8_t* params = raw + raw_stride - 16 - BN * (D / kGroup) * 4;
+      uint8_t* raw = sm + G::kRawAt + e * raw_stride;
+      uint8_t* params = raw + raw_stride - 16 - BN * (D / kGroup) * 4;
       const int t0 = w.t0 + (n >> 1) * BN;
       // which of the lane's four tokens count
       uint32_t live = 0;
@@ -571,14 +663,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int before = n - kSlots;                       // the tile that was in the slot
       if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
-      if (P.fp8) decode_tile<D, 0>(raw, params, ln, live, dst);
-      else if (bits == 8)
-        decode_tile<D, 8>(raw, reinterpret_cast<const uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
-                                   ((static_cast<int64_t>(ms->raw_block[e]) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
-                                       (D / kGroup * 4),
-                          ln, live, dst);
-      else if (bits == 2) decode_tile<D, 2>(raw, params, ln, live, dst);
-      else decode_tile<D, 4>(raw, params, ln, live, dst);
+      if (FP8) decode_tile<D, 0>(raw, params, ln, live, dst, kind == 1, t0, ms);
+      else if (bits == 8) {
+        uint8_t* global = reinterpret_cast<uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
+                          ((static_cast<int64_t>(ms->raw_block[e]) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
+                              (D / kGroup * 4);
+        const bool odd = kind == 1 && odd_groups<D, 255>(global, nullptr, dw, lane, t0, end, ms);
+        decode_tile<D, 8>(raw, global, ln, live, dst, odd, t0, ms);
+      } else if (bits == 2) {
+        if (kind == 1) odd_groups<D, 3>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
+        decode_tile<D, 2>(raw, params, ln, live, dst, false, t0, ms);
+      } else {                                             // (or no block: nothing is live)
+        if (kind == 1) odd_groups<D, 15>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
+        decode_tile<D, 4>(raw, params, ln, live, dst, false, t0, ms);
+      }
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -750,10 +848,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     result.m = top;
     result.poison = result.poison || other.z != 0.0f;
     const int r = w.r0 + (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
-    const bool fine = ok && !result.poison && result.l > 0.0f;
+    if (ms->odd_last >= 0) {
+      const int pos = w.len + min(r, w.rv - 1) / w.g;
+      const int seen = a.plan.window > 0 ? max(0, pos - a.plan.window + 1) : 0;
+      for (int t = max(ms->odd_first, seen); t <= min(ms->odd_last, pos); ++t)
+        if (odd_token<D>(P, table, w.h, t)) result.l = NAN;
+    }
+    // (a sum that is NaN: a query or a seen token is not finite; then so is the row)
+    const bool fine = ok && !result.poison && !(result.l <= 0.0f);
     if (partials > 1 && r < w.rv && side == 0)
       a.ws_ml[part + (MODE == 1 ? group : 0) * all_rows + (static_cast<int64_t>(w.b) * w.T + r / w.g) * hq + w.h * w.g + r % w.g] =
-          make_float2(!ok ? 0.0f : result.l > 0.0f ? result.m : -INFINITY, ok && !result.poison ? result.l : -1.0f);
+          make_float2(!ok ? 0.0f : !(result.l <= 0.0f) ? result.m : -INFINITY, ok && !result.poison ? result.l : -1.0f);
     if (result.any) {
       const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 128;
       const float f = partials > 1 ? 1.0f : (fine ? 1.0f / result.l : 0.0f);
@@ -858,7 +963,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
       }
     }
   }
-  const float f = L > 0.0f ? 1.0f / L : 0.0f;
+  const float f = L <= 0.0f ? 0.0f : 1.0f / L;
   const int64_t at = b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 4) {
@@ -876,7 +981,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
   }
 }
 
-template <int MODE>
+template <int MODE, bool FP8>
 cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
   using G = Geo<MODE>;
   const q4kv_extend_plan& p = a.plan;
@@ -888,12 +993,12 @@ cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
   const int n_raw = min(kMaxRaw, static_cast<int>(G::kRawRing / stride));
   constexpr uint32_t kSmem = smem_bytes<MODE>();
   cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, extend_kernel<MODE>);
+  cudaError_t e = cudaFuncGetAttributes(&attr, extend_kernel<MODE, FP8>);
   if (e != cudaSuccess) return e;
   if (attr.numRegs != kRegs) return cudaErrorInvalidKernelImage;   // the register shares would not add up
-  e = cudaFuncSetAttribute(extend_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(extend_kernel<MODE, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(extend_kernel<MODE>, dim3(static_cast<unsigned>(x), p.n_kv_heads, p.batch), dim3(kThreads), kSmem, stream, a,
+  e = launch_pdl(extend_kernel<MODE, FP8>, dim3(static_cast<unsigned>(x), p.n_kv_heads, p.batch), dim3(kThreads), kSmem, stream, a,
                  stride, n_raw);
   if (e != cudaSuccess) return e;
   const int partials = p.n_splits * G::STREAMS;
@@ -908,8 +1013,12 @@ cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   const q4kv_extend_plan& p = a.plan;
   const ExtendShape sh = extend_shape(p.head_dim, static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads));
-  if (p.head_dim == 256) return launch_mode<2>(a, stream);
-  return sh.rows == 256 ? launch_mode<0>(a, stream) : launch_mode<1>(a, stream);
+  if (a.pool.fp8) {
+    if (p.head_dim == 256) return launch_mode<2, true>(a, stream);
+    return sh.rows == 256 ? launch_mode<0, true>(a, stream) : launch_mode<1, true>(a, stream);
+  }
+  if (p.head_dim == 256) return launch_mode<2, false>(a, stream);
+  return sh.rows == 256 ? launch_mode<0, false>(a, stream) : launch_mode<1, false>(a, stream);
 }
 
 }  // namespace q4kv

@@ -165,6 +165,54 @@ def test_garbage_behind_the_mask_and_the_end_stays_out(d):
     assert out.device == dev
 
 
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("width,fp8", [(4, False), (8, False), (2, False), (8, True)])
+@pytest.mark.parametrize("T,d,window,splits", [(5, 128, 0, 0), (40, 128, 50, 3), (300, 128, 0, 1), (70, 256, 0, 2), (70, 256, 33, 1)])
+def test_tokens_that_are_not_finite_reach_only_the_rows_that_see_them(which, width, fp8, T, d, window, splits):
+    # one token in the cached part, one among the new ones, one of the other
+    # sequence remapped: rows that do not see them keep every bit
+    c = Case([200, 131], T, 4, 2, d, "fp16", widths=(width,), fp8=fp8, rotated=not fp8, seed=T, evict=[(1, 60)])
+    plan = q4.ExtendPlan(2, T, 4, 2, d, c.tables.shape[1], window=window, n_splits=splits)
+    clean = c.run(plan=plan, window=window)
+    odd = {0: [170, 200 + T // 2], 1: [60]}
+    for b, tokens in odd.items():
+        for t in tokens:
+            blk, slot = int(c.tables[b][t // 256]), t % 256
+            if fp8:
+                getattr(c.pool, f"{which}_codes8")[blk, 1, slot, 77] = 0x7F
+            else:
+                getattr(c.pool, f"{which}_params{width}")[blk, 1, slot, 0, slot % 2] = float("inf" if slot % 3 else "nan")
+    got = c.run(plan=plan, window=window)
+    sees = torch.zeros(2, T, 4, dtype=torch.bool)
+    for i in range(T):
+        sees[0, i, 2:] = any(t <= 200 + i and (window == 0 or t > 200 + i - window) for t in odd[0])
+    assert bool(sees.any()) and not bool(sees.all())
+    sees = sees.to(got.device)
+    assert bool(torch.isnan(got[sees]).all())
+    assert torch.equal(got[~sees], clean[~sees])
+
+
+@pytest.mark.parametrize("width", [4, 8, 2])
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (20, 256)])
+def test_the_largest_finite_values(T, d, width):
+    # a group from -65504 to 65504: its rounded scale may end past fp16
+    dev = cuda()
+    lens = [40]
+    c = Case(lens, T, 4, 2, d, "fp16", widths=(width,), seed=T, rotated=False)
+    m = lens[0] + T
+    k, v = W.random_small(m, 2, d, "fp16", seed=T, scale=1.0)
+    v[::3, :, 5], v[::3, :, 9] = 65504.0, -65504.0
+    ids = c.tables[0][:1].tolist()
+    c.pool.quantize(k.to(dev), v.to(dev), torch.tensor(ids, dtype=torch.int32, device=dev))
+    c.ref.quantize_blocks(host(k)[0], host(v)[0], "fp16", ids)
+    want, bound = c.want()
+    # One step less of the scale moves a value by at most 2^-10 of the group's
+    # range, 128.  Only the bound per element is asked for: REL supposes values of
+    # the output's size, and here values of 65504 cancel to outputs of 1800, which
+    # 128 exceeds by 2^-4 of their size.
+    _attend_close(c.run(), want, bound + 2.0 ** -10 * 2 * 65504, rel=2.0 ** -3)
+
+
 @pytest.mark.parametrize("T,d", [(3, 128), (40, 256), (200, 128)])
 def test_split_counts_agree(T, d):
     c = Case([1500, 3, 900], T, 8, 2, d, "fp16", n_new=[T, T - 1, 0], seed=T)
