@@ -13,6 +13,16 @@
 // same in every group, so the (cos, sin) row is read once per item.  With
 // pairs (f, f + rot/2) the partner channels sit in another lane of the same
 // head and come as 8 shuffles of the raw 16-bit words.
+//
+// Bound by latency: each item looks up its length, block, positions and angles
+// before it can turn a row, and the 32 registers of angles beside the encoder's
+// leave room for 16 warps per SM with heads of 256.  8191 tokens of 16 query and
+// 8 KV heads of 256, bf16, take 80 us, 2.8 TB/s of the 220 MB that have to move
+// (34 us at the copy bandwidth; issue 43 %, 22 % of the warps resident).  With a
+// read-back of the chunk behind it, blocks of 256 threads at 3 per SM, which
+// spill, took 116 instead of 109 us there, but 62.5 instead of 68.6 us for
+// 4 x 2048 tokens of 32 and 8 heads of 128 on three axes, so only heads of 128
+// ask for 3.  Keys and values loaded before the look-ups: 132 us (155 registers).
 #include "encode.cuh"
 #include "extend_internal.cuh"
 
@@ -72,7 +82,7 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8]) {
 }
 
 template <int D, typename InT, bool ROT, bool INTER>
-__global__ void __launch_bounds__(256) append_rotary_kernel(const __grid_constant__ RotaryAppendArgs a, int per) {
+__global__ void __launch_bounds__(256, D == 128 ? 3 : 2) append_rotary_kernel(const __grid_constant__ RotaryAppendArgs a, int per) {
   using S = Shape<D>;
   griddep_wait();
   griddep_launch_dependents();
