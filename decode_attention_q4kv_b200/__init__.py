@@ -684,6 +684,8 @@ def extend_attention(pool: Q4KVPool, q: torch.Tensor, block_tables: torch.Tensor
     dev = _same_device(pool.mask, q, block_tables, seq_lens, n_new, workspace, out)
     _check_chunk(q, "q")
     B, T, hq, d = q.shape
+    if d != pool.head_dim:
+        raise ValueError(f"q must have heads of {pool.head_dim}")
     tab, lens, nn = _sequences(B, block_tables, seq_lens, n_new)
     if plan is None:
         with torch.cuda.device(dev):

@@ -67,6 +67,7 @@ q4kv_status q4kv_append_rotary(const q4kv_pool* pool, const q4kv_rotary* rotary,
     if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
         !rows_ok(q_out, q_out_seq_stride, q_out_token_stride, row, 2))
       return Q4KV_ERR_INVALID_ARG;
+    if (batch > 1 && q_out_seq_stride < row) return Q4KV_ERR_INVALID_ARG;   // rows on top of one another
     if (q == q_out && (q_seq_stride != q_out_seq_stride || q_token_stride != q_out_token_stride))
       return Q4KV_ERR_INVALID_ARG;
     a.q = q;
@@ -253,6 +254,7 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
       !rows_ok(out, out_seq_stride, out_token_stride, row, out_dtype == Q4KV_F32 ? 4 : 2))
     return Q4KV_ERR_INVALID_ARG;
+  if (plan->batch > 1 && out_seq_stride < row) return Q4KV_ERR_INVALID_ARG;   // rows on top of one another
   if (block_tables == nullptr || !aligned(block_tables, 4) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
       (n_new != nullptr && !aligned(n_new, 4)))
     return Q4KV_ERR_INVALID_ARG;

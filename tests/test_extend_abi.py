@@ -69,6 +69,7 @@ def test_attention_refusals():
     assert _attend(qdt=2) == BAD and _attend(odt=3) == BAD and _attend(scale=float("nan")) == BAD
     assert _attend(q=None) == BAD and _attend(q=FAKE + 8) == BAD and _attend(out=None) == BAD and _attend(out=FAKE + 2) == BAD
     assert _attend(qs=(7 * 4096, 4095)) == BAD and _attend(qs=(7 * 4096 + 4, 4096)) == BAD and _attend(os_=(7 * 4096, 1024)) == BAD
+    assert _attend(os_=(0, 4096)) == BAD and _attend(os_=(4088, 4096)) == BAD     # rows on top of one another
     assert _attend(tab=None) == BAD and _attend(tab=FAKE + 2) == BAD and _attend(lens=None) == BAD and _attend(nn=FAKE + 2) == BAD
     assert _attend(pool=_pool(n_q4_blocks=0)) == BAD
     assert _attend(pool=_pool(n_kv_heads=4)) == BAD                # the plan's heads are not the pool's
@@ -108,6 +109,7 @@ def test_append_rotary_refusals():
     assert _append(dt=2) == BAD and _append(k=FAKE + 8) == BAD and _append(ts=1028) == BAD and _append(lens=None) == BAD
     assert _append(hq=0) == BAD and _append(qo=None) == BAD and _append(q=FAKE + 2) == BAD and _append(pos=FAKE + 2) == BAD
     assert _append(qs=(16384, 4092)) == BAD and _append(os_=(16384 + 2, 4096)) == BAD
+    assert _append(os_=(4088, 4096)) == BAD and _append(os_=(0, 4096)) == BAD     # rows on top of one another
     assert _append(qo=FAKE, os_=(20480, 4096)) == BAD              # in place with other strides
     assert _append(pool=_pool(n_q4_blocks=0)) == BAD
     assert _append(B=0) == 0 and _append(T=0) == 0

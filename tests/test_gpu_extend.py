@@ -390,6 +390,23 @@ def test_attention_arguments_are_checked(bad):
         q4.extend_attention(c.pool, q, tab, lens, **kw)
 
 
+def test_heads_of_another_size_and_rows_on_top_of_one_another_are_refused():
+    dev = cuda()
+    c = Case([10, 20], 3, 8, 2, 128, "fp16")
+    tab, lens = c.dev(c.tables), c.dev(c.lens)
+    plan = q4.ExtendPlan(2, 3, 8, 2, 128, tab.shape[1])
+    for d in (64, 256):
+        q = torch.zeros(2, 3, 32, d, dtype=torch.float16, device=dev)[:, :, :8]   # rows far enough apart for heads of 128
+        with pytest.raises(ValueError):
+            q4.extend_attention(c.pool, q, tab, lens, plan=plan)
+    one = torch.zeros(1, 3, 8, 128, dtype=torch.float16, device=dev)
+    with pytest.raises(q4.Q4KVError):
+        q4.extend_attention(c.pool, c.q.to(dev), tab, lens, plan=plan, out=one.expand(2, 3, 8, 128))
+    same = c.run(q=c.q[:1].to(dev).expand(2, 3, 8, 128))                             # queries may be shared
+    c.q = c.q[:1].expand(2, 3, 8, 128).contiguous()
+    assert torch.equal(same, c.run())
+
+
 # -- rotary append -------------------------------------------------------------
 
 def _table(pairs, n, seed=0):
