@@ -73,17 +73,23 @@ constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 // MODE 1: D = 128, one row tile; the two pairs of softmax groups take alternate
 //         key tiles with their own accumulators (two partial results).
 // MODE 2: D = 256, one row tile, two softmax groups.
+// MODE 3: MODE 1 for up to 32 rows: the tile holds each four times, and each copy
+//         takes 16 of a step's 64 columns (its weights of the others are 0), so
+//         that all four warps of a group have work; the copies are added up at
+//         the end.  16 x 5 tokens on up to 32768, 32/8 heads: 327 -> 295 us.
 template <int MODE>
 struct Geo {
+  static constexpr bool ALT = MODE == 1 || MODE == 3;  // alternate key tiles
+  static constexpr int COPIES = MODE == 3 ? 4 : 1;     // of a row in the tile
   static constexpr int D = MODE == 2 ? 256 : 128;
   static constexpr int BN = MODE == 2 ? 64 : 128;      // tokens of a key tile
   static constexpr int STEPS = BN / kCols;             // softmax steps of a key tile
   static constexpr int QT = MODE == 0 ? 2 : 1;         // row tiles
-  static constexpr int STREAMS = MODE == 1 ? 2 : 1;    // partial results of a row
+  static constexpr int STREAMS = ALT ? 2 : 1;    // partial results of a row
   static constexpr int R = 128 * QT;
   static constexpr uint32_t kQ = QT * 128 * D * 2;
   static constexpr uint32_t kRawAt = kQ + kSlots * kTile;
-  static constexpr uint32_t kRawRing = MODE == 1 ? 65600 : 32800;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
+  static constexpr uint32_t kRawRing = ALT ? 65600 : 32800;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
   static constexpr uint32_t kMiscAt = kRawAt + kRawRing;
 };
 
@@ -113,7 +119,7 @@ struct Misc {
 template <int MODE>
 constexpr uint32_t smem_bytes() { return Geo<MODE>::kMiscAt + sizeof(Misc); }
 static_assert(Geo<0>::kMiscAt % 16 == 0 && Geo<1>::kMiscAt % 16 == 0 && Geo<2>::kMiscAt % 16 == 0, "alignment");
-static_assert(smem_bytes<0>() <= 232448 && smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory");
+static_assert(smem_bytes<0>() <= 232448 && smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448 && smem_bytes<3>() <= 232448, "shared memory");
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -150,6 +156,9 @@ __device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Misc* 
   wait(bar, parity, ms);
   __syncwarp();
 }
+
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[8]) { tmem_ld8(addr, r); }
 
 // A decoding lane's place: its first token in the tile and its 32-channel
 // unit; its four tokens lie step() apart.
@@ -431,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 
   // Softmax warps (of a group) with real rows, per accumulator; MODE 0 drops its second row tile
   // when no row is in it.  Steps of 64 columns of each accumulator.
-  const int warps0 = min(4, (w.rv - w.r0 + 31) / 32);
-  const int warps1 = MODE == 2 ? 0 : MODE == 1 ? warps0 : max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32));
+  const int warps0 = G::COPIES == 4 ? 4 : min(4, (w.rv - w.r0 + 31) / 32);
+  const int warps1 = MODE == 2 ? 0 : G::ALT ? warps0 : max(0, min(4, (w.rv - w.r0 - 128 + 31) / 32));
   const int groups = warps1 > 0 ? 2 : 1;
-  const int steps0 = (MODE == 1 ? (w.n + 1) / 2 : w.n) * G::STEPS, steps1 = (MODE == 1 ? w.n / 2 : w.n) * G::STEPS;
+  const int steps0 = (G::ALT ? (w.n + 1) / 2 : w.n) * G::STEPS, steps1 = (G::ALT ? w.n / 2 : w.n) * G::STEPS;
 
   if (tid == 0) {
     for (int i = 0; i < 2 * n_raw; ++i) mbar_init(&ms->raw_full[i], 1);
@@ -470,9 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     using Sh = Shape<D>;
     constexpr int kPasses = G::R / Sh::VPW / 16;           // of a warp
     const int rl = lane / Sh::LPV, j = lane % Sh::LPV;
+    auto in_tile = [](int row) { return G::COPIES == 4 ? row & 31 : row; };
     // (a warp's passes lie 16 apart; the next one's row is on its way meanwhile)
     auto load = [&](int p, uint4 (&in)[2]) {
-      const int rr = w.r0 + (p * 16 + warp) * Sh::VPW + rl;
+      const int rr = w.r0 + in_tile((p * 16 + warp) * Sh::VPW) + rl;
       in[0] = in[1] = make_uint4(0u, 0u, 0u, 0u);
       if (p < kPasses && rr < w.rv) {
         const uint4* src = reinterpret_cast<const uint4*>(
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll 1
     for (int p = 0; p < kPasses; ++p) {
       const int row = (p * 16 + warp) * Sh::VPW + rl;
-      if (w.r0 + (p * 16 + warp) * Sh::VPW >= w.rv) break; // (the whole warp)
+      if (G::COPIES == 1 && w.r0 + (p * 16 + warp) * Sh::VPW >= w.rv) break;   // (the whole warp)
       in[0] = next[0];
       in[1] = next[1];
       load(p + 1, next);
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                        v0 = smem_operand(smem_u32(sm) + G::kQ, BN * 128, 1024);
         // O += P V of step v of accumulator s
         auto pv = [&](int s, int v) {
-          const int j = MODE == 1 ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
+          const int j = G::ALT ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
           if (h == 0 && (MODE != 0 || s == 0)) wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);   // first use
           wait(&ms->p_full[s][v & 1], (v >> 1) & 1, ms);
           tc_fence_after();
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         // weights in these buffers were issued before; products of one thread
         // run in order.)
         auto qk = [&](int s, int i) {
-          const int j = MODE == 1 ? 2 * i + s : i, n = 2 * j;
+          const int j = G::ALT ? 2 * i + s : i, n = 2 * j;
           if (MODE != 0 || s == 0) {
             wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
             tc_fence_after();
@@ -703,7 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     regs_up<kSoftRegs>();
     if (group < 2 && (warp & 3) < (group == 0 ? warps0 : warps1)) {
       // ---- softmax -------------------------------------------------------------
-      const int local = (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
+      const int local = (MODE == 0 ? group * 128 : 0) + (G::COPIES == 4 ? 0 : (warp & 3) * 32) + lane;
+      constexpr int kShare = kCols / G::COPIES;            // of a step's columns
+      const int col0 = G::COPIES == 4 ? (warp & 3) * kShare : 0;
       const int r = w.r0 + local;
       const bool real = r < w.rv;
       const int pos = w.len + min(r, w.rv - 1) / w.g;      // the row's position
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int steps = group == 0 ? steps0 : steps1;
       // first token of step k
       auto token = [&](int k) {
-        return w.t0 + (MODE == 1 ? (2 * (k / G::STEPS) + group) * BN + k % G::STEPS * kCols : k * kCols);
+        return w.t0 + (G::ALT ? (2 * (k / G::STEPS) + group) * BN + k % G::STEPS * kCols : k * kCols);
       };
       float m = kNone, l = 0.0f;
       bool poison = false;
@@ -732,24 +744,31 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll 1
       for (int k = side; k < steps; k += 2) {
         const int t0 = token(k);
-        const int hi = pos - t0;                           // last column the row sees
-        const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 : 0;
-        uint32_t x[2][32];
+        const int hi = pos - t0 - col0;                    // last column the row sees
+        const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 - col0 : 0;
+        constexpr int kHalf = kShare / 2;
+        uint32_t x[2][kHalf];
         warp_wait(&ms->s_full[group][side], (k >> 1) & 1, ms);
         tc_fence_after();
-        tmem_ld32(s_at, x[0]);
-        tmem_ld32(s_at + 32, x[1]);
+        tmem_load(s_at + col0, x[0]);
+        tmem_load(s_at + col0 + kHalf, x[1]);
         // (the key decoders wrote this before the tile that the logits come from)
-        const int j = MODE == 1 ? 2 * (k / G::STEPS) + group : k / G::STEPS;
-        const uint2 gone = *reinterpret_cast<const uint2*>(&ms->gone[j & 7][2 * (k % G::STEPS)]);
+        const int j = G::ALT ? 2 * (k / G::STEPS) + group : k / G::STEPS;
+        uint2 gone;
+        if (G::COPIES == 4) {
+          const uint32_t g = reinterpret_cast<const uint16_t*>(&ms->gone[j & 7][2 * (k % G::STEPS)])[warp & 3];
+          gone = make_uint2(g & 0xFFu, g >> 8);
+        } else {
+          gone = *reinterpret_cast<const uint2*>(&ms->gone[j & 7][2 * (k % G::STEPS)]);
+        }
         const bool bad = ms->bad[j & 7] != 0;
         const bool edge = pos_first - t0 < kCols - 1 || (a.plan.window != 0 && pos_last - a.plan.window >= t0);
         tmem_wait_ld(x[0]);
         tmem_wait_ld(x[1]);
-        if (bad && hi >= 0 && lo < kCols) poison = true;
+        if (bad && hi + col0 >= 0 && lo + col0 < kCols) poison = true;
         if ((gone.x | gone.y) != 0) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < kHalf; ++i) {
             if ((gone.x >> i) & 1u) x[0][i] = __float_as_uint(sent);
             if ((gone.y >> i) & 1u) x[1][i] = __float_as_uint(sent);
           }
@@ -757,11 +776,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         if (edge) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int h1 = hi - 32 * c, l1 = lo - 32 * c;
+            const int h1 = hi - kHalf * c, l1 = lo - kHalf * c;
             uint32_t seen = h1 >= 31 ? 0xffffffffu : (h1 < 0 ? 0u : (2u << h1) - 1u);
             seen &= l1 <= 0 ? 0xffffffffu : (l1 > 31 ? 0u : 0xffffffffu << l1);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < kHalf; ++i)
               if (!((seen >> i) & 1u)) x[c][i] = __float_as_uint(-INFINITY);
           }
         }
@@ -769,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
 #pragma unroll
         for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(x[q & 1][q >> 1]), __uint_as_float(x[q & 1][(q >> 1) + 2]));
 #pragma unroll
-        for (int i = 4; i < 32; i += 4)
+        for (int i = 4; i < kHalf; i += 4)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             mx[q] = max3(mx[q], __uint_as_float(x[q & 1][i + (q >> 1)]), __uint_as_float(x[q & 1][i + 2 + (q >> 1)]));
@@ -808,18 +827,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         const float2 off2 = make_float2(kShift - m, kShift - m);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kShare / 8; ++c) {
           uint32_t p[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = 4 * c + i;
-            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[at >> 4][(2 * at) & 31]), __uint_as_float(x[at >> 4][(2 * at + 1) & 31])),
+            const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[2 * at / kHalf][2 * at % kHalf]), __uint_as_float(x[2 * at / kHalf][2 * at % kHalf + 1])),
                                         rs2, off2);
             const float2 q = make_float2(exp2_fast(e.x), exp2_fast(e.y));
             sum[i & 1] = __fadd2_rn(sum[i & 1], q);
             p[i] = h2u(__floats2half2_rn(q.x, q.y));
           }
-          tmem_st4(s_at + 4 * c, p);
+          tmem_st4(s_at + col0 / 2 + 4 * c, p);
+        }
+        if (G::COPIES == 4) {
+          const uint32_t zero[8] = {};
+#pragma unroll
+          for (int q = 1; q < 4; ++q) tmem_st8(s_at + 8 * (((warp & 3) + q) & 3), zero);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
@@ -860,7 +884,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     result.l = result.l * exp2_fast(result.m - top) + other.y * exp2_fast(other.x - top);
     result.m = top;
     result.poison = result.poison || other.z != 0.0f;
-    const int r = w.r0 + (MODE == 0 ? group * 128 : 0) + (warp & 3) * 32 + lane;
+    const int r = w.r0 + (MODE == 0 ? group * 128 : 0) + (G::COPIES == 4 ? 0 : (warp & 3) * 32) + lane;
+    float copy = 1.0f;       // this copy's accumulator goes by its own reference
+    if (G::COPIES == 4) {
+      float l = 0.0f, m = kNone;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = fmaxf(m, told[(group * 2 + (q & 1)) * 128 + (q >> 1) * 32 + lane].x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 one = told[(group * 2 + (q & 1)) * 128 + (q >> 1) * 32 + lane];
+        l += one.y * exp2_fast(one.x - m);
+      }
+      copy = exp2_fast(result.m - m);
+      result.m = m;
+      result.l = l;
+    }
     if (ms->odd_last >= 0) {
       const int pos = w.len + min(r, w.rv - 1) / w.g;
       const int seen = a.plan.window > 0 ? max(0, pos - a.plan.window + 1) : 0;
@@ -869,12 +907,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     // (a sum that is NaN: a query or a seen token is not finite; then so is the row)
     const bool fine = ok && !result.poison && !(result.l <= 0.0f);
-    if (partials > 1 && r < w.rv && side == 0)
-      a.ws_ml[part + (MODE == 1 ? group : 0) * all_rows + (static_cast<int64_t>(w.b) * w.T + r / w.g) * hq + w.h * w.g + r % w.g] =
+    if (partials > 1 && r < w.rv && side == 0 && (G::COPIES == 1 || (warp & 3) == 0))
+      a.ws_ml[part + (G::ALT ? group : 0) * all_rows + (static_cast<int64_t>(w.b) * w.T + r / w.g) * hq + w.h * w.g + r % w.g] =
           make_float2(!ok ? 0.0f : !(result.l <= 0.0f) ? result.m : -INFINITY, ok && !result.poison ? result.l : -1.0f);
     if (result.any) {
       const uint32_t o_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + group * 128;
-      const float f = partials > 1 ? 1.0f : (fine ? 1.0f / result.l : 0.0f);
+      const float f = partials > 1 ? copy : (fine ? 1.0f / result.l : 0.0f);
       uint8_t* mine = stage + (group * 128 + (warp & 3) * 32 + lane) * (pieces * 16);
 #pragma unroll 1
       for (int c = side * (D / 64); c < (side + 1) * (D / 64); ++c) {
@@ -905,15 +943,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   __syncthreads();
   {
     const int rows = w.rv - w.r0;
-    for (int x = warp; x < (MODE == 1 && steps1 > 0 ? 2 : 1) * rows; x += kThreads / 32) {
-      const int s = MODE == 1 && x >= rows ? 1 : 0, q = x - s * rows, r = w.r0 + q;
+    for (int x = warp; x < (G::ALT && steps1 > 0 ? 2 : 1) * rows; x += kThreads / 32) {
+      const int s = G::ALT && x >= rows ? 1 : 0, q = x - s * rows, r = w.r0 + q;
       const int i = r / w.g, head = w.h * w.g + r % w.g;
       uint8_t* dst;
       if (partials > 1) dst = reinterpret_cast<uint8_t*>(a.ws_o + (part + s * all_rows + (static_cast<int64_t>(w.b) * w.T + i) * hq + head) * D);
       else dst = static_cast<uint8_t*>(a.out) + (w.b * a.o_seq_stride + i * a.o_token_stride + static_cast<int64_t>(head) * D) * (wide ? 4 : 2);
-      const uint8_t* src = stage + (MODE == 1 ? s * 128 + q : q) * (pieces * 16);
-      for (int e = lane; e < pieces; e += 32)
-        reinterpret_cast<uint4*>(dst)[e] = *reinterpret_cast<const uint4*>(src + (e ^ (q & 7)) * 16);
+      const uint8_t* src = stage + (G::ALT ? s * 128 + q : q) * (pieces * 16);
+      for (int e = lane; e < pieces; e += 32) {
+        uint4 v = *reinterpret_cast<const uint4*>(src + (e ^ (q & 7)) * 16);
+        if (G::COPIES == 4) {
+          float4 y = *reinterpret_cast<const float4*>(&v);
+#pragma unroll
+          for (int c = 1; c < 4; ++c) {
+            const float4 o = *reinterpret_cast<const float4*>(src + c * 32 * (pieces * 16) + (e ^ (q & 7)) * 16);
+            y = make_float4(y.x + o.x, y.y + o.y, y.z + o.z, y.w + o.w);
+          }
+          v = *reinterpret_cast<const uint4*>(&y);
+        }
+        reinterpret_cast<uint4*>(dst)[e] = v;
+      }
     }
   }
   if (tid == 0 && ms->abort != 0) raise_error(P.error_word, Q4KV_DEVERR_TIMEOUT);
@@ -1025,13 +1074,16 @@ cudaError_t launch_mode(const ExtendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   const q4kv_extend_plan& p = a.plan;
-  const ExtendShape sh = extend_shape(p.head_dim, static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads));
+  const int64_t group_rows = static_cast<int64_t>(p.max_new) * (p.n_q_heads / p.n_kv_heads);
+  const ExtendShape sh = extend_shape(p.head_dim, group_rows);
   if (a.pool.fp8) {
     if (p.head_dim == 256) return launch_mode<2, true>(a, stream);
-    return sh.rows == 256 ? launch_mode<0, true>(a, stream) : launch_mode<1, true>(a, stream);
+    if (sh.rows == 256) return launch_mode<0, true>(a, stream);
+  return group_rows <= 32 ? launch_mode<3, true>(a, stream) : launch_mode<1, true>(a, stream);
   }
   if (p.head_dim == 256) return launch_mode<2, false>(a, stream);
-  return sh.rows == 256 ? launch_mode<0, false>(a, stream) : launch_mode<1, false>(a, stream);
+  if (sh.rows == 256) return launch_mode<0, false>(a, stream);
+  return group_rows <= 32 ? launch_mode<3, false>(a, stream) : launch_mode<1, false>(a, stream);
 }
 
 }  // namespace q4kv
