@@ -56,8 +56,7 @@ namespace {
 constexpr int kDecodeWarp0 = 16, kMmaWarp = 24, kFeedWarp = 25;
 constexpr int kThreads = 28 * 32;
 // Registers: 72 a thread at launch, shared out anew by role.
-constexpr int kRegs = 72, kSoftRegs = 88, kDecodeRegs = 48, kOtherRegs = 56;
-static_assert(16 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 28 * kRegs, "register shares");
+constexpr int kRegs = 72, kOtherRegs = 56;
 constexpr float kNone = -1.0e30f; // reference maximum of a row that has seen nothing
 constexpr int kCols = 64;        // logit columns of a softmax step
 constexpr int kSlots = 4;        // decoded tiles
@@ -76,11 +75,16 @@ constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 // MODE 3: MODE 1 for up to 32 rows: the tile holds each four times, and each copy
 //         takes 16 of a step's 64 columns (its weights of the others are 0), so
 //         that all four warps of a group have work; the copies are added up at
-//         the end.  16 x 5 tokens on up to 32768, 32/8 heads: 327 -> 295 us.
+//         the end.  16 x 5 tokens on up to 32768, 32/8 heads: 327 -> 279 us.
 template <int MODE>
 struct Geo {
   static constexpr bool ALT = MODE == 1 || MODE == 3;  // alternate key tiles
   static constexpr int COPIES = MODE == 3 ? 4 : 1;     // of a row in the tile
+  // Registers of a softmax and of a decoding thread.  With 16 columns a thread the
+  // softmax needs fewer, and a lane can decode its four tokens at once
+  // (16 x 5 tokens on up to 32768: 297 -> 279 us).
+  static constexpr int kSoftRegs = MODE == 3 ? 64 : 88, kDecodeRegs = MODE == 3 ? 96 : 48, kAtOnce = MODE == 3 ? 4 : 1;
+  static_assert(16 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 28 * kRegs, "register shares");
   static constexpr int D = MODE == 2 ? 256 : 128;
   static constexpr int BN = MODE == 2 ? 64 : 128;      // tokens of a key tile
   static constexpr int STEPS = BN / kCols;             // softmax steps of a key tile
@@ -255,14 +259,14 @@ __device__ __noinline__ bool odd_token(const PoolView& P, const int32_t* table, 
 // that their latencies overlap.  A token that does not count takes scale and
 // zero 0 (whatever its own are), so its values are 0.  With `check` 8-bit codes
 // are looked at for values that are not finite, as below.  BITS 0: E4M3 bytes.
-template <int D, int BITS>
+template <int D, int BITS, int AT_ONCE>
 __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* params, const Lane& ln, uint32_t live,
                                             uint8_t* dst, bool check, int t0, Misc* ms) {
   constexpr int W = BITS == 0 ? 8 : BITS;              // words of 32 codes
   constexpr int TS = Lane::step(D);
   constexpr int ROW = D / 8 * W;                       // bytes of a token
   const uint8_t* src = raw + ln.t * ROW + ln.u * 4 * W;
-#pragma unroll 1
+#pragma unroll AT_ONCE
   for (int it = 0; it < 4; ++it) {
     const uint8_t* p = src + it * TS * ROW;
     uint32_t w[W], sz = 0;
@@ -644,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     __syncwarp();
   } else if (warp >= kDecodeWarp0) {
-    regs_down<kDecodeRegs>();
+    if (G::kDecodeRegs > kRegs) regs_up<G::kDecodeRegs>();
+    else regs_down<G::kDecodeRegs>();
     // ---- decode ----------------------------------------------------------------
     const int dw = warp & 3, kind = (warp - kDecodeWarp0) >> 2;
     // a warp takes 8 tokens x 128 channels or 4 x 256 at a time, a lane 32
@@ -686,19 +691,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int before = n - kSlots;                       // the tile that was in the slot
       if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
-      if (FP8) decode_tile<D, 0>(raw, params, ln, live, dst, kind == 1, t0, ms);
+      if (FP8) decode_tile<D, 0, G::kAtOnce>(raw, params, ln, live, dst, kind == 1, t0, ms);
       else if (bits == 8) {
         uint8_t* global = reinterpret_cast<uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
                           ((static_cast<int64_t>(ms->raw_block[e]) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
                               (D / kGroup * 4);
         const bool odd = kind == 1 && odd_groups<D, 255>(global, nullptr, dw, lane, t0, end, ms);
-        decode_tile<D, 8>(raw, global, ln, live, dst, odd, t0, ms);
+        decode_tile<D, 8, G::kAtOnce>(raw, global, ln, live, dst, odd, t0, ms);
       } else if (bits == 2) {
         if (kind == 1) odd_groups<D, 3>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
-        decode_tile<D, 2>(raw, params, ln, live, dst, false, t0, ms);
+        decode_tile<D, 2, G::kAtOnce>(raw, params, ln, live, dst, false, t0, ms);
       } else {                                             // (or no block: nothing is live)
         if (kind == 1) odd_groups<D, 15>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
-        decode_tile<D, 4>(raw, params, ln, live, dst, false, t0, ms);
+        decode_tile<D, 4, G::kAtOnce>(raw, params, ln, live, dst, false, t0, ms);
       }
       fence_async_shared();
       __syncwarp();
@@ -710,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if ((f += 2) >= 2 * n_raw) f -= 2 * n_raw, lap ^= 1;
     }
   } else {
-    regs_up<kSoftRegs>();
+    if (G::kSoftRegs > kRegs) regs_up<G::kSoftRegs>();
+    else regs_down<G::kSoftRegs>();
     if (group < 2 && (warp & 3) < (group == 0 ? warps0 : warps1)) {
       // ---- softmax -------------------------------------------------------------
       const int local = (MODE == 0 ? group * 128 : 0) + (G::COPIES == 4 ? 0 : (warp & 3) * 32) + lane;

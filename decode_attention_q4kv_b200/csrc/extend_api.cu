@@ -165,13 +165,13 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
     // Time in SM cycles: CTAs (one per SM at a time), each with its key tiles and
     // what starting and ending it costs, and the partial results written and
     // read again.  The figures are fitted to times measured with forced split
-    // counts: 4200 cycles a step of 128 tokens x 256 rows, 5000 of 256 x 128,
+    // counts: 4200 cycles a step of 128 tokens x 256 rows, 5000 of 256 x 128 (4300 of 256 x 32),
     // 2400 of 64 x 128 (heads of 256), 27000 a CTA, 3300 bytes a cycle.
     // Sequences of one length run in waves; of several, a CTA that ends early
     // makes room for the next (three quarters of the work, and half of the last
     // CTA's as a tail).  Which it will be is not known here, so a batch is
     // planned for the mean of both.
-    const double step_cycles = head_dim == 256 ? 2400.0 : sh.rows == 256 ? 4200.0 : 5000.0;
+    const double step_cycles = head_dim == 256 ? 2400.0 : sh.rows == 256 ? 4200.0 : group_rows <= 32 ? 4300.0 : 5000.0;
     const double partial_cycles = static_cast<double>(batch) * max_new * n_q_heads * head_dim * 8.0 / 3300.0 * sh.streams;
     const int64_t items = max(int64_t{1}, static_cast<int64_t>(batch) * n_kv_heads * ((group_rows + sh.rows - 1) / sh.rows));
     double best = 1e300;

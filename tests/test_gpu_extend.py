@@ -144,6 +144,21 @@ def test_remapped_slots_and_rows_that_see_nothing_live(d):
     _attend_close(out, want, bound)
 
 
+@pytest.mark.parametrize("T,hq,hkv", [(8, 8, 2), (33, 2, 2), (32, 2, 2), (2, 20, 2), (1, 8, 2)])
+@pytest.mark.parametrize("widths,fp8", [((4, 8, 2), False), ((4,), True)])
+@pytest.mark.parametrize("window", [0, 1, 13, 300])
+def test_few_rows(T, hq, hkv, widths, fp8, window):
+    # up to 32 rows of a group share a tile's columns out among copies; 33 do not
+    lens = [517, 3, 64]
+    evict = [(0, t) for t in range(0, 517, 5)] + [(0, t) for t in range(384, 400)] + [(2, t) for t in range(64)]
+    c = Case(lens, T, hq, hkv, 128, "fp16", widths=widths, fp8=fp8, n_new=[T, T, max(1, T - 2)], evict=evict, seed=T)
+    want, bound = c.want(window=window)
+    for s in (1, 0, 2):
+        plan = q4.ExtendPlan(3, T, hq, hkv, 128, c.tables.shape[1], window=window, n_splits=s)
+        _attend_close(c.run(window=window, plan=plan), want, bound, what=f"splits {s}")
+    assert c.pool.read_device_error() == 0
+
+
 @pytest.mark.parametrize("d", [128, 256])
 def test_garbage_behind_the_mask_and_the_end_stays_out(d):
     # NaN scales in remapped slots, in slots past the end and in blocks past the
