@@ -233,7 +233,9 @@ __device__ __forceinline__ bool tame_group(uint32_t& sz) {
 // Some byte is an E4M3 NaN.
 __device__ __forceinline__ bool fp8_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
-// Whether the value of token t, which is not remapped, is finite.
+// Whether token t is live and its value not finite.  (This and mend_groups are
+// calls, rarely made, kept out of the loops' code; they use 30 and 15 registers,
+// fewer than any role's share.)
 template <int D>
 __device__ __noinline__ bool odd_token(const PoolView& P, const int32_t* table, int h, int t) {
   const int blk = __ldg(table + t / kBlockTokens), slot = t % kBlockTokens;
