@@ -109,6 +109,7 @@ struct Misc {
   uint64_t turn[2][4];     // by accumulator and quarter of its rows: the reference after a step is known
   uint32_t tmem;
   int abort;
+  int issued;              // tiles that the feed has sent for
   // Block of the tile in a ring entry, -1 = an id out of range or no tile yet.  One
   // word, so that a decoder whose wait gave up still finds a block of this pool.
   int raw_block[kMaxRaw];
@@ -146,8 +147,8 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<co
 
 // Bounded wait.  When it runs out, abort is set and this and every later wait of
 // the block returns at once: the roles walk their loops to the end (every access
-// stays inside its buffers whatever they hold), the rows are written as 0 and
-// the error bit is raised.  No sleep between tries: every wait here is short and
+// stays inside its buffers whatever they hold), the block waits for what is still
+// in flight, the rows are written as 0 and the error bit is raised.  No sleep between tries: every wait here is short and
 // on the critical path of the next role.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Misc* ms) {
   if (phase_done(bar, parity)) return;
@@ -591,8 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
             bulk_g2s(dst + raw_stride - 16, P.mask + static_cast<int64_t>(blk) * kMaskWords + (t % kBlockTokens) / 128 * 4, 16, full);
           }
         }
-        if (*reinterpret_cast<volatile int*>(&ms->abort) != 0)      // let the copies in flight land
-          for (int c = max(0, n - n_raw); c < n; ++c) mbar_wait(&ms->raw_full[c % (2 * n_raw)], (c / (2 * n_raw)) & 1);
+        ms->issued = n;
       }
     } else if (warp == kMmaWarp) {
       // ---- product -------------------------------------------------------------
@@ -645,10 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
               for (int h = 0; h < G::STEPS; ++h) pv(s, (i - kAhead) * G::STEPS + h);
             if (i < tiles) qk(s, i);
           }
-        if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) {    // let the products in flight end
-          mma_commit(&ms->spare);
-          mbar_wait(&ms->spare, 0);
-        }
       }
     }
     __syncwarp();
@@ -874,6 +870,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();         // every product is done: the places of the tiles, packed and decoded, are free
+  // Or somebody's wait gave up (no role waits any more, so all threads see the
+  // same): the copies and products in flight are waited for here, where no role
+  // can give up behind them.  A place was filled again only after its copy had been
+  // seen to land, so only the last n_raw copies can be on their way.
+  if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) {
+    if (warp == kFeedWarp && elect_one())
+      for (int c = max(0, ms->issued - n_raw); c < ms->issued; ++c) mbar_wait(&ms->raw_full[c % (2 * n_raw)], (c / (2 * n_raw)) & 1);
+    if (warp == kMmaWarp && elect_one()) {
+      mma_commit(&ms->spare);
+      mbar_wait(&ms->spare, 0);
+    }
+    __syncthreads();
+  }
   tc_fence_after();
   // what the groups of the same rows have, in the packed tiles' place
   float4* told = reinterpret_cast<float4*>(sm + G::kRawAt);
