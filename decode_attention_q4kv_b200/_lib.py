@@ -108,6 +108,9 @@ _EXTEND_SIGNATURES = {
     "q4kv_extend_attention": (c_int32, [P(PoolDesc), P(ExtendPlan), c_void_p, c_int32, c_int64, c_int64, c_void_p,
                                         c_void_p, c_void_p, c_float, c_void_p, c_int32, c_int64, c_int64, c_void_p,
                                         c_size_t, c_void_p]),
+    "q4kv_selftest_extend_wait": (c_int32, [P(PoolDesc), P(ExtendPlan), c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                            c_void_p, c_void_p, c_float, c_void_p, c_int32, c_int64, c_int64, c_void_p,
+                                            c_size_t, c_int32, c_void_p]),
 }
 
 _lib = None

@@ -66,7 +66,6 @@ constexpr int kMaxRaw = 7;
 constexpr float kShift = 6.0f;   // weights are stored times 2^6
 constexpr float kLazy = 8.0f;    // growth of the maximum (log2) that moves it
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr unsigned kTries = 1u << 24;   // tries of one wait: seconds
 
 // MODE 0: D = 128, two row tiles of 128, two softmax groups each.
 // MODE 1: D = 128, one row tile; the two pairs of softmax groups take alternate
@@ -150,16 +149,20 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<co
 // stays inside its buffers whatever they hold), the block waits for what is still
 // in flight, the rows are written as 0 and the error bit is raised.  No sleep between tries: every wait here is short and
 // on the critical path of the next role.
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Misc* ms) {
+struct Gate {
+  Misc* ms;
+  unsigned tries;          // of one wait
+};
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, Gate g) {
   if (phase_done(bar, parity)) return;
-  for (unsigned i = 1; i < kTries; ++i) {
+  for (unsigned i = 1; i < g.tries; ++i) {
     if (phase_done(bar, parity)) return;
-    if ((i & 1023u) == 0 && *reinterpret_cast<volatile int*>(&ms->abort) != 0) return;
+    if ((i & 1023u) == 0 && *reinterpret_cast<volatile int*>(&g.ms->abort) != 0) return;
   }
-  *reinterpret_cast<volatile int*>(&ms->abort) = 1;
+  *reinterpret_cast<volatile int*>(&g.ms->abort) = 1;
 }
-__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Misc* ms) {
-  wait(bar, parity, ms);
+__device__ __forceinline__ void warp_wait(uint64_t* bar, uint32_t parity, Gate g) {
+  wait(bar, parity, g);
   __syncwarp();
 }
 
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   griddep_launch_dependents();
   const PoolView& P = a.pool;
   Misc* ms = reinterpret_cast<Misc*>(sm + G::kMiscAt);
+  const Gate gate{ms, a.tries};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Item w = item_of<MODE>(a);
   const int hq = a.plan.n_q_heads, S = a.plan.n_splits, mb = a.plan.max_blocks_per_seq;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     }
     mbar_init(&ms->spare, 1);
     for (int i = 0; i < 8; ++i) mbar_init(&ms->turn[i >> 2][i & 3], 1);
-    ms->abort = 0;
+    ms->abort = a.tries == 0;
     ms->odd_first = 0x7fffffff;
     ms->odd_last = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
           const int blk = __ldg(table + t / kBlockTokens);
           if (++e == n_raw) e = 0, lap ^= 1;
           if (++f == 2 * n_raw) f = 0;
-          wait(&ms->raw_empty[e], lap ^ 1, ms);
+          wait(&ms->raw_empty[e], lap ^ 1, gate);
           if (*reinterpret_cast<volatile int*>(&ms->abort) != 0) break;
           uint64_t* full = &ms->raw_full[f];
           uint8_t* dst = sm + G::kRawAt + e * raw_stride;
@@ -603,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         // O += P V of step v of accumulator s
         auto pv = [&](int s, int v) {
           const int j = G::ALT ? 2 * (v / G::STEPS) + s : v / G::STEPS, h = v % G::STEPS, n = 2 * j + 1;
-          if (h == 0 && (MODE != 0 || s == 0)) wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);   // first use
-          wait(&ms->p_full[s][v & 1], (v >> 1) & 1, ms);
+          if (h == 0 && (MODE != 0 || s == 0)) wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, gate);   // first use
+          wait(&ms->p_full[s][v & 1], (v >> 1) & 1, gate);
           tc_fence_after();
           const uint32_t p = tmem + kSBase + s * (2 * kCols) + (v & 1) * kCols;
           const uint64_t vd = v0 + (((n % kSlots) * kTile + h * (kCols * 128)) >> 4);
@@ -619,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         auto qk = [&](int s, int i) {
           const int j = G::ALT ? 2 * i + s : i, n = 2 * j;
           if (MODE != 0 || s == 0) {
-            wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, ms);
+            wait(&ms->kv_full[n % kSlots], (n / kSlots) & 1, gate);
             tc_fence_after();
           }
           const uint64_t qd = q0 + (MODE == 0 ? s * (128 * D * 2 >> 4) : 0), kd = k0 + ((n % kSlots) * kTile >> 4);
@@ -664,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     int e = kind, f = kind;                                // n % n_raw, n % (2 n_raw)
     uint32_t lap = 0;                                      // parity of n / (2 n_raw)
     for (int n = kind; n < 2 * w.n; n += 2) {
-      warp_wait(&ms->raw_full[f], lap, ms);
+      warp_wait(&ms->raw_full[f], lap, gate);
       const int blk = __shfl_sync(0xffffffffu, ms->raw_block[e], 0);   // (the warp takes one branch even where a wait gave up)
       const int bits = blk < 0 ? 0 : P.bits_of(blk);
       uint8_t* raw = sm + G::kRawAt + e * raw_stride;
@@ -691,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         if (lane == 0) ms->bad[j] = bits == 0;
       }
       const int before = n - kSlots;                       // the tile that was in the slot
-      if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, ms);
+      if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, gate);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
       if (FP8) decode_tile<D, 0, G::kAtOnce>(raw, params, ln, live, dst, kind == 1, t0, ms);
       else if (bits == 8) {
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         const int lo = a.plan.window > 0 ? pos - a.plan.window + 1 - t0 - col0 : 0;
         constexpr int kHalf = kShare / 2;
         uint32_t x[2][kHalf];
-        warp_wait(&ms->s_full[group][side], (k >> 1) & 1, ms);
+        warp_wait(&ms->s_full[group][side], (k >> 1) & 1, gate);
         tc_fence_after();
         tmem_load(s_at + col0, x[0]);
         tmem_load(s_at + col0 + kHalf, x[1]);
@@ -804,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
         // the reference after the step before, which the other group settles
         float ref = kNone;
         if (k > 0) {
-          warp_wait(turn, (k - 1) & 1, ms);
+          warp_wait(turn, (k - 1) & 1, gate);
           ref = *reinterpret_cast<volatile float*>(reference);
         }
         if (__any_sync(0xffffffffu, real && top > ref + kLazy)) {
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
           const float to = fmaxf(ceilf(fmaxf(ref, top)), kNone);
           if (k > 0) {
             const float f = __int_as_float((static_cast<int>(fmaxf(ref - to, -127.0f)) + 127) << 23);
-            warp_wait(&ms->o_done[group][side ^ 1], ((k - 1) >> 1) & 1, ms);
+            warp_wait(&ms->o_done[group][side ^ 1], ((k - 1) >> 1) & 1, gate);
             tc_fence_after();
 #pragma unroll 1
             for (int e = 0; e < D / 8; ++e) {
@@ -861,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       }
       // The last product: the group that made its weights has seen the product
       // two before it, as a wait on that barrier has to.
-      if (steps > 0 && ((steps - 1) & 1) == side) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, ms);
+      if (steps > 0 && ((steps - 1) & 1) == side) warp_wait(&ms->o_done[group][(steps - 1) & 1], ((steps - 1) >> 1) & 1, gate);
       result.m = m;
       result.l = l;
       result.poison = poison;

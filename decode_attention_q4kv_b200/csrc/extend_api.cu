@@ -229,11 +229,12 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
                    plan);
 }
 
-q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan* plan, const void* q, int32_t q_dtype,
-                                  int64_t q_seq_stride, int64_t q_token_stride, const int32_t* block_tables,
-                                  const int32_t* seq_lens, const int32_t* n_new, float softmax_scale, void* out,
-                                  int32_t out_dtype, int64_t out_seq_stride, int64_t out_token_stride, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+// tries: of one wait of the chunk kernel (the decode kernel takes no such limit).
+static q4kv_status extend_attention(const q4kv_pool* pool, const q4kv_extend_plan* plan, const void* q, int32_t q_dtype,
+                                    int64_t q_seq_stride, int64_t q_token_stride, const int32_t* block_tables,
+                                    const int32_t* seq_lens, const int32_t* n_new, float softmax_scale, void* out,
+                                    int32_t out_dtype, int64_t out_seq_stride, int64_t out_token_stride, void* workspace,
+                                    size_t workspace_bytes, unsigned tries, void* stream) {
   q4kv_status st = check_pool(pool);
   if (st != Q4KV_OK) return st;
   if (plan == nullptr) return Q4KV_ERR_INVALID_ARG;
@@ -265,7 +266,7 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(plan->head_dim));
   // (the decode kernel wants aligned tables and numbers rows of codes in 32 bits)
   const int64_t widest = max(pool->n_q4_blocks, max(pool->n_q8_blocks, pool->n_q2_blocks));
-  if (plan->decode_splits > 0 && n_new == nullptr && (plan->batch == 1 || (q_seq_stride == row && out_seq_stride == row)) &&
+  if (tries == kTries && plan->decode_splits > 0 && n_new == nullptr && (plan->batch == 1 || (q_seq_stride == row && out_seq_stride == row)) &&
       aligned(block_tables, 16) && widest * pool->n_kv_heads * kBlockTokens < (int64_t{1} << 31)) {
     q4kv_decode_plan d;
     st = q4kv_decode_plan_make(plan->batch, plan->n_q_heads, plan->n_kv_heads, plan->head_dim, plan->max_blocks_per_seq,
@@ -304,6 +305,7 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
   a.out_dtype = out_dtype;
   a.o_seq_stride = out_seq_stride;
   a.o_token_stride = out_token_stride;
+  a.tries = tries;
   a.ws_o = static_cast<float*>(workspace);
   const size_t partial_rows = static_cast<size_t>(plan->batch) * plan->max_new * plan->n_q_heads * plan->n_splits *
                               extend_shape(plan->head_dim, static_cast<int64_t>(plan->max_new) *
@@ -313,6 +315,28 @@ q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan*
                                             round_up(partial_rows * plan->head_dim * sizeof(float), 256))
                 : nullptr;
   return from_cuda(launch_extend(a, as_stream(stream)));
+}
+
+q4kv_status q4kv_extend_attention(const q4kv_pool* pool, const q4kv_extend_plan* plan, const void* q, int32_t q_dtype,
+                                  int64_t q_seq_stride, int64_t q_token_stride, const int32_t* block_tables,
+                                  const int32_t* seq_lens, const int32_t* n_new, float softmax_scale, void* out,
+                                  int32_t out_dtype, int64_t out_seq_stride, int64_t out_token_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return extend_attention(pool, plan, q, q_dtype, q_seq_stride, q_token_stride, block_tables, seq_lens, n_new,
+                          softmax_scale, out, out_dtype, out_seq_stride, out_token_stride, workspace, workspace_bytes,
+                          kTries, stream);
+}
+
+q4kv_status q4kv_selftest_extend_wait(const q4kv_pool* pool, const q4kv_extend_plan* plan, const void* q,
+                                      int32_t q_dtype, int64_t q_seq_stride, int64_t q_token_stride,
+                                      const int32_t* block_tables, const int32_t* seq_lens, const int32_t* n_new,
+                                      float softmax_scale, void* out, int32_t out_dtype, int64_t out_seq_stride,
+                                      int64_t out_token_stride, void* workspace, size_t workspace_bytes, int32_t tries,
+                                      void* stream) {
+  if (tries < 0 || static_cast<unsigned>(tries) >= kTries) return Q4KV_ERR_INVALID_ARG;
+  return extend_attention(pool, plan, q, q_dtype, q_seq_stride, q_token_stride, block_tables, seq_lens, n_new,
+                          softmax_scale, out, out_dtype, out_seq_stride, out_token_stride, workspace, workspace_bytes,
+                          static_cast<unsigned>(tries), stream);
 }
 
 }  // extern "C"

@@ -54,7 +54,9 @@ struct ExtendArgs {
   int64_t o_seq_stride, o_token_stride;
   float* ws_o;   // [splits][batch * max_new * n_q_heads][D]
   float2* ws_ml; // [splits][batch * max_new * n_q_heads] (reference maximum, sum)
+  unsigned tries;  // of one wait of a block, after which it gives up
 };
+constexpr unsigned kTries = 1u << 24;   // seconds
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream);
 
 // How the chunk kernel cuts its work: a CTA takes `rows` query rows (token,

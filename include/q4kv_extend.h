@@ -156,6 +156,19 @@ q4kv_status q4kv_extend_attention(const q4kv_pool *pool, const q4kv_extend_plan 
                                   int32_t out_dtype, int64_t out_seq_stride, int64_t out_token_stride, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/*
+ * Diagnostic: q4kv_extend_attention by the chunk kernel with `tries` (0 <= tries
+ * < 2^24, the kernel's own limit) tries of each wait inside it before the block
+ * gives up.  Where one gives up, the block's rows are written as 0 and
+ * Q4KV_DEVERR_TIMEOUT is raised; with 0 every block counts as having given up.
+ */
+q4kv_status q4kv_selftest_extend_wait(const q4kv_pool *pool, const q4kv_extend_plan *plan, const void *q,
+                                      int32_t q_dtype, int64_t q_seq_stride, int64_t q_token_stride,
+                                      const int32_t *block_tables, const int32_t *seq_lens, const int32_t *n_new,
+                                      float softmax_scale, void *out, int32_t out_dtype, int64_t out_seq_stride,
+                                      int64_t out_token_stride, void *workspace, size_t workspace_bytes, int32_t tries,
+                                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif
