@@ -109,9 +109,11 @@ struct Misc {
   uint32_t tmem;
   int abort;
   int issued;              // tiles that the feed has sent for
-  // Block of the tile in a ring entry, -1 = an id out of range or no tile yet.  One
+  // What is in a ring entry: 16 times the index of the tile's block among those of
+  // its code width, plus the width; 0 = a block id out of range or no tile yet.  One
   // word, so that a decoder whose wait gave up still finds a block of this pool.
-  int raw_block[kMaxRaw];
+  // (2^28 blocks of one width would be terabytes.)
+  uint32_t raw_what[kMaxRaw];
   // Remapped slots of key tile j and whether its block id is out of range, at
   // j % 8, from the key decoders to the softmax.  (When tile j + 8 is decoded,
   // the keys of tile j + 6 are used up, and the softmax is past tile j.)
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     for (int i = 0; i < 2 * n_raw; ++i) mbar_init(&ms->raw_full[i], 1);
     for (int i = 0; i < n_raw; ++i) {
       mbar_init(&ms->raw_empty[i], 4);
-      ms->raw_block[i] = -1;
+      ms->raw_what[i] = 0;
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&ms->kv_full[i], 4);
     for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&ms->kv_empty[i], 1);
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
           uint8_t* dst = sm + G::kRawAt + e * raw_stride;
           if (blk < 0 || blk >= P.n_blocks()) {
             raise_error(P.error_word, Q4KV_DEVERR_BLOCK_ID);
-            ms->raw_block[e] = -1;
+            ms->raw_what[e] = 0;
             mbar_arrive(full);
           } else {
             const int bits = P.bits_of(blk);
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
                                               : (bits == 8 ? (key ? P.k_params8 : P.v_params8) : (key ? P.k_params2 : P.v_params2));
             // (the scales of 8-bit codes stay in global memory: the ring has no room for them)
             const uint32_t cb = BN * D / 8 * bits, pb = bits == 8 ? 0 : BN * (D / kGroup) * 4;
-            ms->raw_block[e] = blk;
+            ms->raw_what[e] = static_cast<uint32_t>(phys) << 4 | static_cast<uint32_t>(bits);
             mbar_arrive_tx(full, cb + pb + 16);
             bulk_g2s(dst, codes + row * (D / 8 * bits), cb, full);
             if (pb > 0) bulk_g2s(dst + raw_stride - 16 - BN * (D / kGroup) * 4, params + row * (D / kGroup), pb, full);
@@ -669,8 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     uint32_t lap = 0;                                      // parity of n / (2 n_raw)
     for (int n = kind; n < 2 * w.n; n += 2) {
       warp_wait(&ms->raw_full[f], lap, gate);
-      const int blk = __shfl_sync(0xffffffffu, ms->raw_block[e], 0);   // (the warp takes one branch even where a wait gave up)
-      const int bits = blk < 0 ? 0 : P.bits_of(blk);
+      const uint32_t what = __shfl_sync(0xffffffffu, ms->raw_what[e], 0);   // (one branch for the warp, even where a wait gave up)
+      const int bits = what & 15u;
       uint8_t* raw = sm + G::kRawAt + e * raw_stride;
       uint8_t* params = raw + raw_stride - 16 - BN * (D / kGroup) * 4;
       const int t0 = w.t0 + (n >> 1) * BN;
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       if (FP8) decode_tile<D, 0, G::kAtOnce>(raw, params, ln, live, dst, kind == 1, t0, ms);
       else if (bits == 8) {
         uint8_t* global = reinterpret_cast<uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
-                          ((static_cast<int64_t>(blk - P.n_q4) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
+                          ((static_cast<int64_t>(what >> 4) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
                               (D / kGroup * 4);
         const bool odd = kind == 1 && odd_groups<D, 255>(global, nullptr, dw, lane, t0, end, ms);
         decode_tile<D, 8, G::kAtOnce>(raw, global, ln, live, dst, odd, t0, ms);
