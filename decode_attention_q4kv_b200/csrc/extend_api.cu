@@ -20,6 +20,22 @@ bool rows_ok(const void* p, int64_t seq_stride, int64_t token_stride, int64_t ro
          (token_stride * size) % 16 == 0;
 }
 
+// No two rows of such an array share memory (token_stride >= row).  Sequence
+// after sequence and token after token are seen at once; other interleavings
+// row by row: rows b and i apart by less than a row's length in one axis come
+// back by a whole number of steps of the other.
+bool rows_apart(int64_t seq_stride, int64_t token_stride, int64_t row, int64_t batch, int64_t max_new) {
+  if (batch <= 1 || seq_stride >= (max_new - 1) * token_stride + row) return true;
+  if (seq_stride >= row && token_stride >= (batch - 1) * seq_stride + row) return true;
+  if (seq_stride < row) return false;
+  for (int64_t b = 1; b < batch; ++b) {
+    const int64_t at = b * seq_stride, i = at / token_stride;   // neighbours of sequence b's first row
+    if (i < max_new && at - i * token_stride < row) return false;
+    if (i + 1 < max_new && (i + 1) * token_stride - at < row) return false;
+  }
+  return true;
+}
+
 // The checks every call makes of its pool (q4kv_block_image_stride makes them
 // and computes a size on the host).
 q4kv_status check_pool(const q4kv_pool* pool) {
@@ -67,7 +83,7 @@ q4kv_status q4kv_append_rotary(const q4kv_pool* pool, const q4kv_rotary* rotary,
     if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
         !rows_ok(q_out, q_out_seq_stride, q_out_token_stride, row, 2))
       return Q4KV_ERR_INVALID_ARG;
-    if (batch > 1 && q_out_seq_stride < row) return Q4KV_ERR_INVALID_ARG;   // rows on top of one another
+    if (!rows_apart(q_out_seq_stride, q_out_token_stride, row, batch, max_new)) return Q4KV_ERR_INVALID_ARG;
     if (q == q_out && (q_seq_stride != q_out_seq_stride || q_token_stride != q_out_token_stride))
       return Q4KV_ERR_INVALID_ARG;
     a.q = q;
@@ -255,7 +271,7 @@ static q4kv_status extend_attention(const q4kv_pool* pool, const q4kv_extend_pla
   if (!rows_ok(q, q_seq_stride, q_token_stride, row, 2) ||
       !rows_ok(out, out_seq_stride, out_token_stride, row, out_dtype == Q4KV_F32 ? 4 : 2))
     return Q4KV_ERR_INVALID_ARG;
-  if (plan->batch > 1 && out_seq_stride < row) return Q4KV_ERR_INVALID_ARG;   // rows on top of one another
+  if (!rows_apart(out_seq_stride, out_token_stride, row, plan->batch, plan->max_new)) return Q4KV_ERR_INVALID_ARG;
   if (block_tables == nullptr || !aligned(block_tables, 4) || seq_lens == nullptr || !aligned(seq_lens, 4) ||
       (n_new != nullptr && !aligned(n_new, 4)))
     return Q4KV_ERR_INVALID_ARG;

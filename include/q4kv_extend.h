@@ -56,9 +56,9 @@ typedef struct {
  *                itself with equal strides, and overlap it in no other way
  *   positions    device int32 [n_axes][batch][max_new], or NULL: token i of
  *                sequence b is at seq_lens[b] + i on every axis
- * q, q_out and the strides keep the alignment rules of k and v; with several
- * sequences q_out_seq_stride >= n_q_heads*D.  q_out rows of
- * tokens at or past n_new[b] are written as 0.  A token whose position lies
+ * q, q_out and the strides keep the alignment rules of k and v; no two rows of
+ * q_out may share memory.  q_out rows of tokens at or past n_new[b] are written
+ * as 0.  A token whose position lies
  * outside the table raises Q4KV_DEVERR_POSITION; it is not cached and its
  * q_out row is 0, as for a length or block id out of range.
  */
@@ -132,9 +132,8 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  *   n_new        device int32 [batch], 0 <= n_new[b] <= max_new; NULL =
  *                max_new for every sequence
  *   block_tables device int32 [batch][max_blocks_per_seq]
- *   out          as q, of out_dtype (F32, F16 or BF16), its own strides (with
- *                several sequences out_seq_stride >= n_q_heads*D); must not
- *                overlap q
+ *   out          as q, of out_dtype (F32, F16 or BF16), its own strides; no
+ *                two of its rows may share memory, nor may it overlap q
  *   softmax_scale <= 0 selects 1/sqrt(D)
  *   workspace    as for q4kv_decode_attention
  * Token i of sequence b sees the positions t <= seq_lens[b] + i and, with

@@ -1,0 +1,33 @@
+"""Host-only checks of the calls of include/q4kv_extend.h: strides and arguments
+that would make a kernel write one place twice, or read or write past an array, are
+refused before a device is touched."""
+import itertools
+
+import pytest
+
+from decode_attention_q4kv_b200 import _lib
+from test_abi import _pool
+from test_extend_abi import _append, _attend, _plan
+
+BAD = _lib.ERR_INVALID_ARG
+
+
+def _share(ss, ts, row, B, T):
+    at = sorted(b * ss + i * ts for b in range(B) for i in range(T))
+    return any(y - x < row for x, y in zip(at, at[1:]))
+
+
+@pytest.mark.parametrize("B,T", [(2, 2), (2, 7), (3, 2), (5, 3), (4, 1), (1, 5)])
+def test_output_rows_that_share_memory_are_refused(B, T):
+    # one KV head of 128: rows of 128, strides in eighths of a row
+    pool, plan = _pool(n_kv_heads=1), _plan(B=B, T=T, hq=1, hkv=1, mb=4, splits=1)[1]
+    assert plan.workspace_bytes > 0            # the check behind that of the rows: a good call ends there
+    kinds = set()
+    for ss, ts in itertools.product(range(0, 9 * 128, 16), range(128, 9 * 128, 16)):
+        shared = _share(ss, ts, 128, B, T)
+        kinds.add(shared)
+        kw = dict(qs=(128 * T, 128), os_=(ss, ts))
+        assert _attend(pool=pool, plan=plan, **kw) == (BAD if shared else _lib.ERR_WORKSPACE), (ss, ts)
+        if shared:
+            assert _append(pool=pool, B=B, T=T, ss=128 * T, ts=128, hq=1, **kw) == BAD, (ss, ts)
+    assert kinds == ({False} if B == 1 else {False, True})

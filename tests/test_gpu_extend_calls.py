@@ -1,0 +1,22 @@
+"""Calls of the operators that extend a cached prompt as they may be made, each
+against the definitions: layouts, strides and arguments at their edges."""
+import numpy as np
+import pytest
+import torch
+
+import decode_attention_q4kv_b200 as q4
+from helpers import cuda
+from test_gpu_extend import Case, _attend_close
+
+pytestmark = pytest.mark.gpu
+
+
+def test_output_rows_token_after_token():
+    # [T][B][Hq][D] in memory: a sequence's rows lie between those of the others
+    dev = cuda()
+    c = Case([40, 300, 7], 9, 8, 2, 128, "fp16", n_new=[9, 4, 9], seed=3)
+    want, bound = c.want()
+    out = torch.full((9, 3, 8, 128), 7.0, device=dev).transpose(0, 1)
+    _attend_close(c.run(out=out), want, bound)
+    with pytest.raises(q4.Q4KVError):          # neighbours' rows in one place
+        c.run(out=torch.zeros(11 * 8 * 128, device=dev).as_strided((3, 9, 8, 128), (1024, 1024, 128, 1)))
