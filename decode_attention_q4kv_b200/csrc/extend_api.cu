@@ -128,6 +128,12 @@ q4kv_status q4kv_gather_tokens(const q4kv_pool* pool, const int32_t* tables, int
       (starts != nullptr && !aligned(starts, 4)) || k_out == nullptr || v_out == nullptr || !aligned(k_out, 16) ||
       !aligned(v_out, 16))
     return Q4KV_ERR_INVALID_ARG;
+  // keys' and values' rows may lie between one another, not on one another
+  const uintptr_t row = static_cast<uintptr_t>(pool->n_kv_heads) * pool->head_dim * size, step = static_cast<uintptr_t>(out_stride) * size;
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(k_out), va = reinterpret_cast<uintptr_t>(v_out);
+  const uintptr_t apart = ka < va ? va - ka : ka - va;
+  if (apart < static_cast<uintptr_t>(n_rows - 1) * step + row && (apart % step < row || step - apart % step < row))
+    return Q4KV_ERR_INVALID_ARG;
   GatherArgs a;
   a.pool = view_of(*pool);
   a.tables = tables;

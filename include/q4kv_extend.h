@@ -81,7 +81,8 @@ q4kv_status q4kv_append_rotary(const q4kv_pool *pool, const q4kv_rotary *rotary,
  *                offsets[batch]) are left as they were
  *   k_out, v_out device [n_rows][Hkv][D] of out_dtype (F32, F16 or BF16),
  *                16-byte aligned, rows out_stride elements apart
- *                (out_stride >= Hkv*D, a multiple of 16 bytes)
+ *                (out_stride >= Hkv*D, a multiple of 16 bytes); no row of one
+ *                may share memory with a row of the other
  * Values as for q4kv_dequantize (x = fl(code*s + z), rounded once; keys
  * un-rotated when unrotate_k is 1 and the pool stores them rotated; remapped
  * slots read K = -1e4, V = 0).  A token outside its table, or in a block whose

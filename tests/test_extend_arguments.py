@@ -6,8 +6,8 @@ import itertools
 import pytest
 
 from decode_attention_q4kv_b200 import _lib
-from test_abi import _pool
-from test_extend_abi import _append, _attend, _plan
+from test_abi import FAKE, _pool
+from test_extend_abi import _append, _attend, _gather, _plan
 
 BAD = _lib.ERR_INVALID_ARG
 
@@ -31,3 +31,15 @@ def test_output_rows_that_share_memory_are_refused(B, T):
         if shared:
             assert _append(pool=pool, B=B, T=T, ss=128 * T, ts=128, hq=1, **kw) == BAD, (ss, ts)
     assert kinds == ({False} if B == 1 else {False, True})
+
+
+@pytest.mark.parametrize("stride", [128, 192, 256, 400])
+@pytest.mark.parametrize("n", [1, 2, 5])
+def test_key_and_value_rows_that_share_memory_are_refused(stride, n):
+    pool, shared = _pool(n_kv_heads=1), 0
+    for apart in range(-6 * stride, 6 * stride + 1, 8):        # elements of 2 bytes
+        if any(abs(apart + i * stride) < 128 for i in range(1 - n, n)):
+            shared += 1
+            assert _gather(pool=pool, n=n, v=FAKE + 2 * apart, stride=stride) == BAD, apart
+    assert shared > 0
+    assert _gather(pool=pool, n=0, v=FAKE, stride=stride) == 0

@@ -20,3 +20,17 @@ def test_output_rows_token_after_token():
     _attend_close(c.run(out=out), want, bound)
     with pytest.raises(q4.Q4KVError):          # neighbours' rows in one place
         c.run(out=torch.zeros(11 * 8 * 128, device=dev).as_strided((3, 9, 8, 128), (1024, 1024, 128, 1)))
+
+
+@pytest.mark.parametrize("n", [1, 2, 37])
+def test_keys_and_values_read_back_into_one_array(n):
+    # [n][2][Hkv][D]: rows of keys and of values by turns
+    dev = cuda()
+    c = Case([300], 0, 2, 2, 128, "fp16", seed=2)
+    both = torch.full((n, 2, 2, 128), 9.0, dtype=torch.float16, device=dev)
+    args = (c.dev(c.tables), c.dev([200]), c.dev([0, n]), n)
+    k, v = c.pool.gather(*args)
+    c.pool.gather(*args, k_out=both[:, 0], v_out=both[:, 1])
+    assert torch.equal(both[:, 0], k) and torch.equal(both[:, 1], v)
+    with pytest.raises(q4.Q4KVError):
+        c.pool.gather(*args, k_out=k, v_out=k)
