@@ -75,8 +75,11 @@ __device__ __forceinline__ void turn_words(uint32_t (&w)[8], const Turn& t) {
   }
 }
 
+// FIXED: nothing writes the row during the launch.  (Queries may be rotated in place.)
+template <bool FIXED>
 __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8]) {
-  const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+  const uint4* u = static_cast<const uint4*>(p);
+  const uint4 a = FIXED ? __ldg(u) : u[0], b = FIXED ? __ldg(u + 1) : u[1];
   w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
   w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
@@ -177,17 +180,17 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : 2) append_rotary_kernel(co
     if (q0 < g1) {
       const InT* src = static_cast<const InT*>(a.q) + b * a.q_seq_stride + i * a.q_token_stride + j * kEPL;
       InT* dst = static_cast<InT*>(a.q_out) + b * a.o_seq_stride + i * a.o_token_stride + j * kEPL;
-      // lanes past the last head read a real row, store nothing
-      auto head = [&](int g) { return min((g - kv_groups) * S::VPW + r, hq - 1); };
+      // (lanes past the last head load and store nothing)
+      auto head = [&](int g) { return (g - kv_groups) * S::VPW + r; };
       uint32_t w[8] = {}, next[8] = {};
-      if (ok) load_words(src + static_cast<int64_t>(head(q0)) * D, next);
+      if (ok && head(q0) < hq) load_words<false>(src + static_cast<int64_t>(head(q0)) * D, next);
 #pragma unroll 1
       for (int gi = q0; gi < g1; ++gi) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = next[e];
-        if (ok && gi + 1 < g1) load_words(src + static_cast<int64_t>(head(gi + 1)) * D, next);
+        if (ok && gi + 1 < g1 && head(gi + 1) < hq) load_words<false>(src + static_cast<int64_t>(head(gi + 1)) * D, next);
         if (ok) turn_words<InT, INTER>(w, t);
-        if ((gi - kv_groups) * S::VPW + r < hq) {
+        if (head(gi) < hq) {
           uint4* o = reinterpret_cast<uint4*>(dst + static_cast<int64_t>(head(gi)) * D);
           o[0] = make_uint4(w[0], w[1], w[2], w[3]);
           o[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -202,8 +205,8 @@ __global__ void __launch_bounds__(256, D == 128 ? 3 : 2) append_rotary_kernel(co
       const int hs = valid ? h : hkv - 1;
       const int64_t src = b * a.seq_stride + i * a.token_stride + static_cast<int64_t>(hs) * D + j * kEPL;
       uint32_t wk[8], wv[8];
-      load_words(static_cast<const InT*>(a.k) + src, wk);
-      load_words(static_cast<const InT*>(a.v) + src, wv);
+      load_words<true>(static_cast<const InT*>(a.k) + src, wk);
+      load_words<true>(static_cast<const InT*>(a.v) + src, wv);
       turn_words<InT, INTER>(wk, t);
       float2 xk[8], xv[8];
       unpack16<InT>(make_uint4(wk[0], wk[1], wk[2], wk[3]), make_uint4(wk[4], wk[5], wk[6], wk[7]), xk);

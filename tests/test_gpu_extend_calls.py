@@ -34,3 +34,30 @@ def test_keys_and_values_read_back_into_one_array(n):
     assert torch.equal(both[:, 0], k) and torch.equal(both[:, 1], v)
     with pytest.raises(q4.Q4KVError):
         c.pool.gather(*args, k_out=k, v_out=k)
+
+
+@pytest.mark.parametrize("d,hq,inter", [(128, 7, False), (128, 40, True), (256, 3, False), (256, 16, True)])
+@pytest.mark.parametrize("T", [3, 900])
+def test_queries_rotated_in_place_inside_a_fused_row(d, hq, inter, T):
+    # q, k and v as slices of one row per token; the last group of heads is not full
+    dev = cuda()
+    g = torch.Generator(device=dev).manual_seed(T)
+    qkv = torch.randn(2, T, hq + 4, d, generator=g, device=dev).to(torch.bfloat16)
+    ro = q4.Rotary(q4.Rotary.make_table(10000.0 ** (-torch.arange(d // 2) / (d // 2)), T + 50, device=dev), interleaved=inter)
+    tab = torch.arange(10, device=dev).view(2, 5)
+    lens, n_new = torch.tensor([7, 40], device=dev), torch.tensor([T, T - 2], device=dev)
+
+    def run(x, in_place):
+        pool = q4.Q4KVPool(2, d, 10, device=dev)
+        q = x[:, :, :hq]
+        o = pool.append_rotary(x[:, :, hq:hq + 2], x[:, :, hq + 2:], ro, tab, lens, n_new, q=q, q_out=q if in_place else None)
+        assert pool.read_device_error() == 0
+        return o, pool
+
+    want, a = run(qkv.clone(), False)
+    for _ in range(3):
+        x = qkv.clone()
+        got, b = run(x, True)
+        assert got.data_ptr() == x.data_ptr() and torch.equal(got, want)
+        assert torch.equal(x[:, :, hq:], qkv[:, :, hq:])
+        assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in ("k_codes4", "k_params4", "v_codes4", "v_params4"))
