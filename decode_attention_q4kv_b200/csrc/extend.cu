@@ -237,6 +237,7 @@ __device__ __forceinline__ bool tame_group(uint32_t& sz) {
   if ((sz & 0x7FFFu) != 0) --sz;
   return finite_group<MAX>(sz);
 }
+constexpr uint32_t kNanGroup = 0x7FFF7FFFu;   // every code of it is NaN
 // Some byte is an E4M3 NaN.
 __device__ __forceinline__ bool fp8_nan(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
@@ -267,10 +268,10 @@ __device__ __noinline__ bool odd_token(const PoolView& P, const int32_t* table, 
 // The lane's four tokens of a tile, 32 channels each.  The loads come first so
 // that their latencies overlap.  A token that does not count takes scale and
 // zero 0 (whatever its own are), so its values are 0.  With `check` 8-bit codes
-// are looked at for values that are not finite, as below.  BITS 0: E4M3 bytes.
+// are looked at for what is not finite, as below.  BITS 0: E4M3 bytes.
 template <int D, int BITS, int AT_ONCE>
 __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* params, const Lane& ln, uint32_t live,
-                                            uint8_t* dst, bool check, int t0, Misc* ms) {
+                                            uint8_t* dst, bool check, bool key, int t0, Misc* ms) {
   constexpr int W = BITS == 0 ? 8 : BITS;              // words of 32 codes
   constexpr int TS = Lane::step(D);
   constexpr int ROW = D / 8 * W;                       // bytes of a token
@@ -303,6 +304,10 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
         on = (odd & 0x80808080u) == 0;
       } else {
         on = tame_group<255>(sz);
+        if (!on && key) {
+          on = true;
+          sz = kNanGroup;
+        }
       }
       if (!on) {
         atomicMin(&ms->odd_first, t0 + ln.t + it * TS);
@@ -327,8 +332,10 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
 
 // A value that is not finite takes 0 as well: a product with it would reach the
 // rows that do not see its token, too (a weight of 0 times it is NaN).  Its
-// place is noted, and the rows that do see it become NaN at the end.  (A key's
-// logits are replaced where they are not seen, so keys need none of this.)
+// place is noted, and the rows that do see it become NaN at the end.  A key's
+// logits are replaced where they are not seen, so a key that is not finite only has
+// to be NaN, for infinities of one sign would give the logit -Inf, and the weight 0.
+// (E4M3 has no infinities.)
 //
 // Whether one of the warp's tokens needs it is found out with one look at their
 // scales, two groups a lane.  Scales in shared memory are put right there, 8-bit
@@ -336,16 +343,17 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
 // to 13 % of whole calls, in a warp of its own, which delays the decoders, 1 to
 // 16 %; here 1 to 4 %, and 7 % for E4M3, whose bytes are looked at themselves.)
 template <int D, int MAX>
-__device__ __noinline__ void mend_groups(uint2* at, uint2 sz, bool live, int t, Misc* ms) {
+__device__ __noinline__ void mend_groups(uint2* at, uint2 sz, bool key, bool live, int t, Misc* ms) {
   const bool fx = tame_group<MAX>(sz.x), fy = tame_group<MAX>(sz.y);
-  *at = make_uint2(fx ? sz.x : 0u, fy ? sz.y : 0u);
-  if (live && !(fx && fy)) {
+  const uint32_t odd = key ? kNanGroup : 0u;
+  *at = make_uint2(fx ? sz.x : odd, fy ? sz.y : odd);
+  if (!key && live && !(fx && fy)) {
     atomicMin(&ms->odd_first, t);
     atomicMax(&ms->odd_last, t);
   }
 }
 template <int D, int MAX>
-__device__ __forceinline__ bool odd_groups(uint8_t* params, const uint8_t* mask, int dw, int lane, int t0, int end, Misc* ms) {
+__device__ __forceinline__ bool odd_groups(uint8_t* params, const uint8_t* mask, bool key, int dw, int lane, int t0, int end, Misc* ms) {
   const int t = D == 128 ? dw * 8 + (lane & 7) + 32 * (lane >> 3) : dw * 4 + ((lane >> 1) & 3) + 16 * (lane >> 3);
   uint2* at = reinterpret_cast<uint2*>(params + t * (D / kGroup) * 4) + (D == 128 ? 0 : lane & 1);
   const uint2 sz = *at;
@@ -353,7 +361,7 @@ __device__ __forceinline__ bool odd_groups(uint8_t* params, const uint8_t* mask,
   if (!__any_sync(0xffffffffu, odd)) return false;
   if (MAX != 255) {
     const int slot = (t0 & 64) * (D / 256) + t;            // within the 128 slots of the mask
-    if (odd) mend_groups<D, MAX>(at, sz, t0 + t < end && !((mask[slot >> 3] >> (slot & 7)) & 1u), t0 + t, ms);
+    if (odd) mend_groups<D, MAX>(at, sz, key, t0 + t < end && !((mask[slot >> 3] >> (slot & 7)) & 1u), t0 + t, ms);
     __syncwarp();
   }
   return true;
@@ -699,19 +707,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int before = n - kSlots;                       // the tile that was in the slot
       if (before >= 0) warp_wait(&ms->kv_empty[before % (2 * kSlots)], (before / (2 * kSlots)) & 1, gate);
       uint8_t* dst = sm + G::kQ + (n % kSlots) * kTile + dst0;
-      if (FP8) decode_tile<D, 0, G::kAtOnce>(raw, params, ln, live, dst, kind == 1, t0, ms);
+      const bool key = kind == 0;
+      if (FP8) decode_tile<D, 0, G::kAtOnce>(raw, params, ln, live, dst, !key, key, t0, ms);
       else if (bits == 8) {
-        uint8_t* global = reinterpret_cast<uint8_t*>(kind == 0 ? P.k_params8 : P.v_params8) +
+        uint8_t* global = reinterpret_cast<uint8_t*>(key ? P.k_params8 : P.v_params8) +
                           ((static_cast<int64_t>(what >> 4) * P.n_kv_heads + w.h) * kBlockTokens + t0 % kBlockTokens) *
                               (D / kGroup * 4);
-        const bool odd = kind == 1 && odd_groups<D, 255>(global, nullptr, dw, lane, t0, end, ms);
-        decode_tile<D, 8, G::kAtOnce>(raw, global, ln, live, dst, odd, t0, ms);
+        const bool odd = odd_groups<D, 255>(global, nullptr, key, dw, lane, t0, end, ms);
+        decode_tile<D, 8, G::kAtOnce>(raw, global, ln, live, dst, odd, key, t0, ms);
       } else if (bits == 2) {
-        if (kind == 1) odd_groups<D, 3>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
-        decode_tile<D, 2, G::kAtOnce>(raw, params, ln, live, dst, false, t0, ms);
+        odd_groups<D, 3>(params, raw + raw_stride - 16, key, dw, lane, t0, end, ms);
+        decode_tile<D, 2, G::kAtOnce>(raw, params, ln, live, dst, false, key, t0, ms);
       } else {                                             // (or no block: nothing is live)
-        if (kind == 1) odd_groups<D, 15>(params, raw + raw_stride - 16, dw, lane, t0, end, ms);
-        decode_tile<D, 4, G::kAtOnce>(raw, params, ln, live, dst, false, t0, ms);
+        odd_groups<D, 15>(params, raw + raw_stride - 16, key, dw, lane, t0, end, ms);
+        decode_tile<D, 4, G::kAtOnce>(raw, params, ln, live, dst, false, key, t0, ms);
       }
       fence_async_shared();
       __syncwarp();

@@ -141,9 +141,12 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  * plan->window > 0, t > seq_lens[b] + i - window.  Remapped slots have logit
  * -1e4 and value 0 as in q4kv_decode_attention; a token that sees remapped
  * slots only returns 0.  Rows at or past n_new[b] are written as 0.  Keys and
- * values are rounded to fp16 (relative 2^-11) for the tensor cores.  A cached
- * key or value that is not finite in fp16 reaches no row that does not see its
- * token; the rows that do become NaN.
+ * values are rounded to fp16 for the tensor cores, by at most 2^-11 of their size
+ * (2^-25 where they are below 2^-14).  Where the rounded scale carries a finite
+ * group past the largest fp16 value, it is lowered by one step, which moves the
+ * group's values by at most 2^-10 of its range.  A token with a key or value
+ * that is not finite in fp16 even so reaches no row that does not see it; the
+ * rows that do become NaN.
  * One new token per sequence (max_new == 1, no window, n_new NULL, rows next to
  * each other) takes the kernel of q4kv_decode_attention, with its accuracy;
  * there a length of -1 is an empty sequence (row 0, no error bit).

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import decode_attention_q4kv_b200 as q4
-from helpers import cuda
+from decode_attention_q4kv_b200 import workloads as W
+from helpers import cuda, host
 from test_gpu_extend import Case, _attend_close
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,44 @@ def test_queries_rotated_in_place_inside_a_fused_row(d, hq, inter, T):
         assert got.data_ptr() == x.data_ptr() and torch.equal(got, want)
         assert torch.equal(x[:, :, hq:], qkv[:, :, hq:])
         assert all(torch.equal(getattr(a, n), getattr(b, n)) for n in ("k_codes4", "k_params4", "v_codes4", "v_params4"))
+
+
+@pytest.mark.parametrize("width", [4, 8, 2])
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (30, 128), (20, 256)])
+def test_the_largest_finite_keys(T, d, width):
+    # a group of raw keys from -65504 to 65504: its rounded scale may end past fp16
+    dev = cuda()
+    scale = 1e-6
+    c = Case([40], T, 4, 2, d, "fp16", widths=(width,), seed=T, rotated=False)
+    k, v = W.random_small(40 + T, 2, d, "fp16", seed=T, scale=1.0)
+    k[::3, :, 5], k[::3, :, 9] = 65504.0, -65504.0
+    ids = c.tables[0][:1].tolist()
+    c.pool.quantize(k.to(dev), v.to(dev), torch.tensor(ids, dtype=torch.int32, device=dev))
+    c.ref.quantize_blocks(host(k)[0], host(v)[0], "fp16", ids)
+    want, bound = c.want(scale=scale)
+    # One step less of the scale moves a key by at most 2^-10 of the group's range,
+    # so a logit by x = scale |q|_1 128 and each weight by a factor of e^(+-2x); the
+    # output, a mean of values within V, then moves by at most (e^2x - 1) 2 V.
+    x = scale * float(c.q.float().abs().sum(-1).max()) * 2.0 ** -10 * 2 * 65504
+    _attend_close(c.run(softmax_scale=scale), want, bound + np.expm1(2 * x) * 2 * float(v.float().abs().max()), rel=1.0)
+
+
+@pytest.mark.parametrize("width,s", [(4, 10000.0), (8, 600.0), (2, 40000.0)])
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (30, 128), (20, 256)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_one_key_channel_past_fp16(T, d, width, s, sign):
+    # the logits of that token are +Inf or -Inf by the query's sign; the rows that see it are NaN either way
+    c = Case([100], T, 4, 2, d, "fp16", widths=(width,), seed=T, rotated=False)
+    c.q[..., 8:] = 0.0
+    c.q[..., :8] = sign
+    clean = c.run()
+    t = 100 + T // 2
+    blk, slot = int(c.tables[0][0]), t
+    codes, params = getattr(c.pool, f"k_codes{width}"), getattr(c.pool, f"k_params{width}")
+    codes[blk, 1, slot] = 0
+    codes[blk, 1, slot, 0] = (1 << width) - 1      # channel 0 alone
+    params[blk, 1, slot, 0, 0], params[blk, 1, slot, 0, 1] = s, 0.0
+    got = c.run()
+    hit = torch.zeros(1, T, 4, dtype=torch.bool, device=got.device)
+    hit[0, T // 2:, 2:] = True
+    assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], clean[~hit])
