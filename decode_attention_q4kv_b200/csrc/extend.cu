@@ -542,9 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       for (int i = 0; i < 8; ++i) m = max3(m, fabsf(x[i].x), fabsf(x[i].y));
 #pragma unroll
       for (int st = 1; st < Sh::LPV; st <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, st));
-      // the row's largest magnitude comes to lie in [64, 128)
+      // the row's largest magnitude comes to lie in [64, 128); a row with an infinity
+      // is NaN (one with a NaN is by itself), so that its logits cannot all be -Inf
       const int e = m == 0.0f ? 0 : min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100), 127);
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
+      const float f = m == INFINITY ? NAN : __uint_as_float(static_cast<uint32_t>(127 + 6 - e) << 23);
       if (j == 0) ms->exponent[row] = static_cast<int8_t>(e);
       uint32_t o[8];
 #pragma unroll

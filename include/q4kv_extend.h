@@ -146,10 +146,11 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  * group past the largest fp16 value, it is lowered by one step, which moves the
  * group's values by at most 2^-10 of its range.  A token with a key or value
  * that is not finite in fp16 even so reaches no row that does not see it; the
- * rows that do become NaN.
+ * rows that do become NaN, as does a row whose query is not finite.
  * One new token per sequence (max_new == 1, no window, n_new NULL, rows next to
  * each other) takes the kernel of q4kv_decode_attention, with its accuracy;
- * there a length of -1 is an empty sequence (row 0, no error bit).
+ * there a length of -1 is an empty sequence (row 0, no error bit), and queries, keys
+ * and values have to be finite.
  * A sequence longer than its table raises Q4KV_DEVERR_SEQ_LEN, a block id out
  * of range Q4KV_DEVERR_BLOCK_ID; the affected rows are written as 0.
  */

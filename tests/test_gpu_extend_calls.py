@@ -103,3 +103,18 @@ def test_one_key_channel_past_fp16(T, d, width, s, sign):
     hit = torch.zeros(1, T, 4, dtype=torch.bool, device=got.device)
     hit[0, T // 2:, 2:] = True
     assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (30, 128), (20, 256)])
+@pytest.mark.parametrize("rotated", [True, False])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_queries_that_are_not_finite_make_their_own_rows_nan(T, d, rotated, bad):
+    c = Case([100], T, 4, 2, d, "bf16", seed=T, rotated=rotated)
+    c.pool.k_params4[:, :, :, 0, 0] = 0.0          # keys of channel 3's group are positive: with raw keys
+    c.pool.k_params4[:, :, :, 0, 1] = 1.0          # every logit has the sign of that channel's query
+    clean = c.run()
+    c.q[0, T // 2, 1, 3] = bad
+    got = c.run()
+    hit = torch.zeros(1, T, 4, dtype=torch.bool, device=got.device)
+    hit[0, T // 2, 1] = True
+    assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], clean[~hit])
