@@ -499,8 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   const int group = MODE == 2 ? warp >> 3 : (warp >> 3) & 1, side = (warp >> 2) & 1;
 
   if (warp < kDecodeWarp0) {
-    // Q: rotate, scale each row by a power of two, round to fp16.  Rows of no
-    // real token are left as they are: no other row depends on them.
+    // Q: rotate, times log2(e) scale, scale each row by a power of two, round to
+    // fp16.  What is left to do to the products is then a power of two, which is
+    // exact, so that logits and the reference maximum differ by what they differ by,
+    // however large both are.  Rows of no real token are left as they are: no other
+    // row depends on them.
     using Sh = Shape<D>;
     constexpr int kPasses = G::R / Sh::VPW / 16;           // of a warp
     const int rl = lane / Sh::LPV, j = lane % Sh::LPV;
@@ -519,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     };
     uint4 in[2], next[2];
     load(0, next);
+    const float qs = a.scale * kLog2e * (P.k_rotated ? kRotScale<D> : 1.0f);
 #pragma unroll 1
     for (int p = 0; p < kPasses; ++p) {
       const int row = (p * 16 + warp) * Sh::VPW + rl;
@@ -530,13 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       float2 x[8];
       if (a.q_dtype == Q4KV_F16) unpack16<__half>(in[0], in[1], x);
       else unpack16<__nv_bfloat16>(in[0], in[1], x);
-      if (P.k_rotated) {
-        rotate_pairs<D>(x, j);
-        if (kRotScale<D> != 1.0f) {
+      if (P.k_rotated) rotate_pairs<D>(x, j);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x * kRotScale<D>, x[i].y * kRotScale<D>);
-        }
-      }
+      for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x * qs, x[i].y * qs);
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max3(m, fabsf(x[i].x), fabsf(x[i].y));
@@ -743,10 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
       const int r = w.r0 + local;
       const bool real = r < w.rv;
       const int pos = w.len + min(r, w.rv - 1) / w.g;      // the row's position
-      // log2(e) * scale * 2^exponent: from products to logits (rows behind the
-      // last real one take its place)
-      const float rs = a.scale * kLog2e *
-                       __uint_as_float(static_cast<uint32_t>(127 - 6 + ms->exponent[min(r, w.rv - 1) - w.r0]) << 23);
+      // 2^exponent: from products to logits (rows behind the last real one take its place)
+      const float rs = __uint_as_float(static_cast<uint32_t>(127 - 6 + ms->exponent[min(r, w.rv - 1) - w.r0]) << 23);
       // positions of the warp's first and last row: a step that all of them see
       // whole needs no mask
       const int pos_first = w.len + (w.r0 + local - lane) / w.g, pos_last = w.len + min(w.r0 + local - lane + 31, w.rv - 1) / w.g;

@@ -118,3 +118,32 @@ def test_queries_that_are_not_finite_make_their_own_rows_nan(T, d, rotated, bad)
     hit = torch.zeros(1, T, 4, dtype=torch.bool, device=got.device)
     hit[0, T // 2, 1] = True
     assert bool(torch.isnan(got[hit]).all()) and torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (30, 128), (20, 256)])
+@pytest.mark.parametrize("power", [16, 30])
+def test_logits_far_below_zero(T, d, power):
+    # every key is a constant, every query -2^power: the least key takes all the weight
+    dev = cuda()
+    c = Case([100], T, 4, 2, d, "bf16", seed=T, rotated=False)
+    k, v = W.random_small(100 + T, 2, d, "bf16", seed=T, scale=1.0)
+    # whole and half numbers, exact in a group's zero, falling towards the end
+    k[:] = (torch.arange(100 + T, 0, -1) / 2.0 + 10.0).view(-1, 1, 1).to(k.dtype)
+    ids = c.tables[0][:1].tolist()
+    c.pool.quantize(k.to(dev), v.to(dev), torch.tensor(ids, dtype=torch.int32, device=dev))
+    c.ref.quantize_blocks(host(k)[0], host(v)[0], "bf16", ids)
+    c.q[:] = -2.0 ** power
+    want, _ = c.want(scale=2.0 ** -3)
+    got = c.run(softmax_scale=2.0 ** -3).cpu().numpy()
+    # the values' rounding to fp16 (weights of 1 are exact)
+    assert np.all(np.abs(got - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (20, 256)])
+@pytest.mark.parametrize("mag,scale", [(2.0 ** -118, 2.0 ** 114.5), (2.0 ** 120, 2.0 ** -123.5), (2.0 ** -110, 1e-20), (1.0, 1e-38)])
+def test_the_ends_of_queries_and_scales(T, d, mag, scale):
+    # products of scale and query of ordinary size, and next to nothing (the mean of what is live)
+    c = Case([100], T, 4, 2, d, "bf16", seed=T, evict=[(0, t) for t in range(0, 100, 7)])
+    c.q = (c.q.float() * mag).to(torch.bfloat16)
+    want, bound = c.want(scale=scale)
+    _attend_close(c.run(softmax_scale=scale), want, bound)
