@@ -57,7 +57,7 @@ constexpr int kDecodeWarp0 = 16, kMmaWarp = 24, kFeedWarp = 25;
 constexpr int kThreads = 28 * 32;
 // Registers: 72 a thread at launch, shared out anew by role.
 constexpr int kRegs = 72, kOtherRegs = 56;
-constexpr float kNone = -1.0e30f; // reference maximum of a row that has seen nothing
+constexpr float kNone = -3.0e38f; // reference maximum of a row that has seen nothing: below every logit
 constexpr int kCols = 64;        // logit columns of a softmax step
 constexpr int kSlots = 4;        // decoded tiles
 constexpr uint32_t kTile = 32768;// bytes of a decoded tile

@@ -121,7 +121,7 @@ def test_queries_that_are_not_finite_make_their_own_rows_nan(T, d, rotated, bad)
 
 
 @pytest.mark.parametrize("T,d", [(6, 128), (150, 128), (30, 128), (20, 256)])
-@pytest.mark.parametrize("power", [16, 30])
+@pytest.mark.parametrize("power", [16, 30, 100, 116])
 def test_logits_far_below_zero(T, d, power):
     # every key is a constant, every query -2^power: the least key takes all the weight
     dev = cuda()
