@@ -156,6 +156,8 @@ static bool one_token(int32_t max_new, int32_t window, int g, int32_t head_dim) 
   return max_new == 1 && window == 0 && g <= 8 && g * head_dim <= 1024;
 }
 
+constexpr int64_t kMaxTokens = 32768;
+
 // decode_splits < 0 lets the decode planner choose from num_sms.
 static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                              int32_t max_blocks, int32_t window, int32_t n_splits, int32_t decode_splits,
@@ -182,6 +184,11 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
   if (window > 0) ctx = min(ctx, static_cast<int64_t>(window) + (sh.rows + g - 1) / g + sh.tile);
   const int64_t step = static_cast<int64_t>(sh.tile) * sh.streams;
   const int64_t steps = (ctx + step - 1) / step;
+  // An accumulator takes at most kMaxTokens tokens: the tensor cores cut off what they
+  // add up in binary32, so a sum of one sign falls short by 6e-9 of itself for every token.
+  // (Values of mean 4 over 524288 tokens in one accumulator came out 3.2e-3 too small,
+  // over 131072 8.1e-4, over 32768 2.0e-4; a rounding to fp16 is 4.9e-4 at most.)
+  const int64_t smin = (steps * sh.tile + kMaxTokens - 1) / kMaxTokens;
   int64_t s = n_splits;
   if (s == 0) {
     // Time in SM cycles: CTAs (one per SM at a time), each with its key tiles and
@@ -197,8 +204,8 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
     const double partial_cycles = static_cast<double>(batch) * max_new * n_q_heads * head_dim * 8.0 / 3300.0 * sh.streams;
     const int64_t items = max(int64_t{1}, static_cast<int64_t>(batch) * n_kv_heads * ((group_rows + sh.rows - 1) / sh.rows));
     double best = 1e300;
-    s = 1;
-    for (int64_t cand = 1; cand <= min(steps, int64_t{4} * num_sms); ++cand) {
+    s = smin;
+    for (int64_t cand = smin; cand <= max(smin, min(steps, int64_t{4} * num_sms)); ++cand) {
       const int64_t per = (steps + cand - 1) / cand;
       if ((steps + per - 1) / per != cand) continue;
       const double one = per * step_cycles + 27000.0;
@@ -214,7 +221,7 @@ static q4kv_status make_plan(int32_t batch, int32_t max_new, int32_t n_q_heads, 
       }
     }
   }
-  s = max(int64_t{1}, min(s, steps));
+  s = max(smin, min(s, steps));
   const int64_t per = (steps + s - 1) / s;
   s = (steps + per - 1) / per;
   memset(plan, 0, sizeof(*plan));

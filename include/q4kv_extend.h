@@ -114,7 +114,9 @@ typedef struct {
 } q4kv_extend_plan;
 
 /*
- * Fill `plan`.  n_splits > 0 forces that split count (clamped to the context);
+ * Fill `plan`.  n_splits > 0 forces that split count, clamped to the context and
+ * to what keeps a partial result at 32768 tokens or less (the tensor cores' sums fall
+ * short by up to 2^-12 of themselves over so many, and by more over more);
  * 0 lets the library choose from num_sms (0 = those of the current device).
  * Supported: head_dim 128 or 256, 1 <= n_q_heads / n_kv_heads <= 64.
  */

@@ -43,3 +43,20 @@ def test_key_and_value_rows_that_share_memory_are_refused(stride, n):
             assert _gather(pool=pool, n=n, v=FAKE + 2 * apart, stride=stride) == BAD, apart
     assert shared > 0
     assert _gather(pool=pool, n=0, v=FAKE, stride=stride) == 0
+
+
+@pytest.mark.parametrize("T,hq,hkv,d,tile,streams", [(512, 8, 2, 128, 128, 1), (16, 8, 2, 128, 128, 2), (4, 8, 2, 128, 128, 2),
+                                                     (64, 16, 8, 256, 64, 1)])
+def test_no_accumulator_takes_more_than_32768_tokens(T, hq, hkv, d, tile, streams):
+    for B, mb in itertools.product((1, 7, 300), (1, 127, 128, 129, 257, 1000, 4096, 131072)):
+        for splits in (0, 1, 2, 5, 1000):
+            st, p = _plan(B=B, T=T, hq=hq, hkv=hkv, d=d, mb=mb, splits=splits)
+            assert st == 0
+            steps = -(-mb * 256 // (tile * streams))
+            assert -(-steps // p.n_splits) * tile <= 32768, (B, mb, splits)
+            again = _plan(B=B, T=T, hq=hq, hkv=hkv, d=d, mb=mb, splits=p.n_splits)[1]
+            assert (again.n_splits, again.workspace_bytes) == (p.n_splits, p.workspace_bytes)
+            if mb <= 128 and splits == 1:
+                assert p.n_splits == 1
+    p = _plan(B=300, T=T, hq=hq, hkv=hkv, d=d, mb=131072, window=4096)[1]
+    assert p.n_splits == 1                     # a window bounds the tokens by itself
