@@ -1,4 +1,4 @@
-"""Chunk attention over long contexts, against 64 bits."""
+"""Chunk attention over long contexts and many partial results, against 64 bits."""
 import math
 
 import pytest
@@ -6,6 +6,7 @@ import torch
 
 import decode_attention_q4kv_b200 as q4
 from helpers import cuda
+from test_gpu_extend import Case, _attend_close
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +43,29 @@ def test_sums_over_long_contexts_do_not_drift(T, hq, hkv, d, n):
         off = float((out[0, i, h].double() - want).norm() / want.norm())
         assert off <= 2.0 ** -12 + 2.0 ** -17, (i, h, plan.n_splits, off)
     assert pool.read_device_error() == 0
+
+
+@pytest.mark.parametrize("T,hq,hkv,d,lens", [(40, 8, 2, 128, [10300, 4000]), (3, 8, 2, 128, [10300, 77]),
+                                             (64, 8, 2, 128, [5200, 300]), (9, 4, 2, 256, [2700, 640])])
+def test_more_than_a_warp_of_partial_results(T, hq, hkv, d, lens):
+    c = Case(lens, T, hq, hkv, d, "fp16", n_new=[T, T - 1], seed=T)
+    plan = q4.ExtendPlan(2, T, hq, hkv, d, c.tables.shape[1], n_splits=10000)    # one step of keys each
+    assert plan.n_splits > 32
+    want, bound = c.want()
+    _attend_close(c.run(plan=plan), want, bound)
+    one = q4.ExtendPlan(2, T, hq, hkv, d, c.tables.shape[1], n_splits=1)
+    assert one.n_splits == 1
+    _attend_close(c.run(plan=one), want, bound)
+
+
+@pytest.mark.parametrize("T,hq,hkv,d", [(70, 8, 2, 128), (300, 4, 2, 128), (70, 8, 2, 256)])
+@pytest.mark.parametrize("widths", [(4, 8, 2), (8, 2), (2, 4)])
+@pytest.mark.parametrize("window", [0, 333])
+def test_mixed_widths_with_more_rows_than_one_tile(T, hq, hkv, d, widths, window):
+    evict = [(0, t) for t in range(0, 700, 9)] + [(1, t) for t in range(256, 330)]
+    c = Case([900, 350], T, hq, hkv, d, "bf16", n_new=[T, T - 7], widths=widths, seed=T, evict=evict)
+    want, bound = c.want(window=window)
+    for s in (0, 1, 3):
+        plan = q4.ExtendPlan(2, T, hq, hkv, d, c.tables.shape[1], window=window, n_splits=s)
+        _attend_close(c.run(plan=plan, window=window), want, bound, what=f"splits {s}")
+    assert c.pool.read_device_error() == 0
