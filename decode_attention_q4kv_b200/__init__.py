@@ -702,6 +702,8 @@ def extend_attention(pool: Q4KVPool, q: torch.Tensor, block_tables: torch.Tensor
     else:
         os_ = _row_strides(out)
     qs = _row_strides(q)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _call(dev, "q4kv_extend_attention", pool._ref, plan._ref, q.data_ptr(), _IN_DTYPES[q.dtype], qs[0], qs[1],
           tab.data_ptr(), lens.data_ptr(), _addr(nn), softmax_scale, out.data_ptr(), _OUT_DTYPES[out.dtype], os_[0], os_[1],

@@ -147,3 +147,18 @@ def test_the_ends_of_queries_and_scales(T, d, mag, scale):
     c.q = (c.q.float() * mag).to(torch.bfloat16)
     want, bound = c.want(scale=scale)
     _attend_close(c.run(softmax_scale=scale), want, bound)
+
+
+def test_a_workspace_that_is_not_one_piece_is_refused():
+    # a byte expanded to the size asked for passes for that many bytes
+    dev = cuda()
+    c = Case([600], 20, 8, 2, 128, "fp16", seed=1)
+    plan = q4.ExtendPlan(1, 20, 8, 2, 128, c.tables.shape[1], n_splits=2)
+    n = plan.workspace_bytes
+    for ws in (torch.zeros(1, dtype=torch.uint8, device=dev).expand(n), torch.zeros(2 * n, dtype=torch.uint8, device=dev)[::2]):
+        with pytest.raises(ValueError):
+            c.run(plan=plan, workspace=ws)
+    with pytest.raises(q4.Q4KVError):
+        c.run(plan=plan, workspace=torch.zeros(n - 1, dtype=torch.uint8, device=dev))
+    want, bound = c.want()
+    _attend_close(c.run(plan=plan, workspace=torch.zeros(n // 4 + 1, dtype=torch.float32, device=dev)), want, bound)
