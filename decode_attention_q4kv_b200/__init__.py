@@ -664,7 +664,16 @@ class ExtendPlan:
         self._shape = (batch, max_new, n_q_heads, max_blocks_per_seq, window)
 
     def __getattr__(self, name):
-        return getattr(self.__dict__["c"], name)
+        if "c" not in self.__dict__:                         # (being copied or unpickled)
+            raise AttributeError(name)
+        return getattr(self.c, name)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._ref = ctypes.byref(self.c)
 
     def workspace(self, device) -> Optional[torch.Tensor]:
         n = self.c.workspace_bytes

@@ -1,9 +1,13 @@
 """Host-only checks of the calls of include/q4kv_extend.h: strides and arguments
 that would make a kernel write one place twice, or read or write past an array, are
 refused before a device is touched."""
+import copy
 import itertools
+import pickle
 
 import pytest
+
+import decode_attention_q4kv_b200 as q4
 
 from decode_attention_q4kv_b200 import _lib
 from test_abi import FAKE, _pool
@@ -60,3 +64,14 @@ def test_no_accumulator_takes_more_than_32768_tokens(T, hq, hkv, d, tile, stream
                 assert p.n_splits == 1
     p = _plan(B=300, T=T, hq=hq, hkv=hkv, d=d, mb=131072, window=4096)[1]
     assert p.n_splits == 1                     # a window bounds the tokens by itself
+
+
+@pytest.mark.parametrize("copied", [copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p))])
+def test_a_plan_can_be_copied(copied):
+    p = q4.ExtendPlan(2, 7, 32, 8, 128, 200, window=5000, n_splits=3, num_sms=148)
+    c = copied(p)
+    assert (c.n_splits, c.workspace_bytes, c.window, c._shape) == (p.n_splits, p.workspace_bytes, p.window, p._shape)
+    assert c._ref._obj is c.c and bytes(c.c) == bytes(p.c)
+    with pytest.raises(AttributeError):
+        c.nothing
+    assert not hasattr(q4.ExtendPlan.__new__(q4.ExtendPlan), "n_splits")
