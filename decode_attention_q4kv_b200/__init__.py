@@ -279,8 +279,8 @@ class Q4KVPool:
         dev = _same_device(self.mask, k, v, tables, seq_lens, n_new, positions, q, q_out, rotary.table)
         _check_chunk(k, "k")
         B, T, hkv, d = k.shape
-        ks = k.stride()
-        if v.dtype != k.dtype or v.shape != k.shape or v.stride() != ks:
+        ks = _row_strides(k)
+        if v.dtype != k.dtype or v.shape != k.shape or not _rows_in_one_piece(v) or _row_strides(v) != ks:
             raise ValueError("k and v must share dtype, shape and strides")
         if hkv != self.n_kv_heads or d != self.head_dim:
             raise ValueError(f"k and v must have {self.n_kv_heads} heads of {self.head_dim}")
@@ -307,7 +307,6 @@ class Q4KVPool:
             qs = _row_strides(q)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        ks = _row_strides(k)
         _call(dev, "q4kv_append_rotary", self._ref, rotary._ref, k.data_ptr(), v.data_ptr(), _IN_DTYPES[k.dtype], B, T,
               _addr(nn), ks[0], ks[1], _addr(q), hq, qs[0], qs[1], _addr(q_out), os_[0], os_[1], tab.data_ptr(),
               tab.shape[1], lens.data_ptr(), _addr(pos))
@@ -400,7 +399,7 @@ class Q4KVPool:
         shape = (int(n_rows), self.n_kv_heads, self.head_dim)
         stride = shape[1] * shape[2]
         for o, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if o is not None and (tuple(o.shape) != shape or o.dtype != out_dtype or o.stride(2) != 1 or o.stride(1) != shape[2]):
+            if o is not None and (tuple(o.shape) != shape or o.dtype != out_dtype or not _rows_in_one_piece(o)):
                 raise ValueError(f"{name} must be {out_dtype} of shape {shape} with contiguous rows")
         if shape[0] > 1:
             given = [o.stride(0) for o in (k_out, v_out) if o is not None]
@@ -430,9 +429,14 @@ class Q4KVPool:
 def _check_chunk(x: torch.Tensor, name: str) -> None:
     if x.dtype not in _IN_DTYPES or x.dim() != 4:
         raise ValueError(f"{name} must be float16 or bfloat16 [B][T][H][D]")
-    s = x.stride()
-    if s[3] != 1 or s[2] != x.shape[3]:
+    if not _rows_in_one_piece(x):
         raise ValueError(f"each token's [H][D] row of {name} must be contiguous")
+
+
+def _rows_in_one_piece(x: torch.Tensor) -> bool:
+    """Whether the last two axes are contiguous (one of one head has no stride of its own)."""
+    s = x.stride()
+    return s[-1] == 1 and (s[-2] == x.shape[-1] or x.shape[-2] == 1)
 
 
 def _row_strides(x: torch.Tensor) -> Tuple[int, int]:
@@ -706,7 +710,7 @@ def extend_attention(pool: Q4KVPool, q: torch.Tensor, block_tables: torch.Tensor
     if out is None:
         out = torch.empty((B, T, hq, d), dtype=out_dtype, device=q.device)
         os_ = (T * hq * d, hq * d)
-    elif out.shape != q.shape or out.dtype not in _OUT_DTYPES or out.stride(3) != 1 or out.stride(2) != d:
+    elif out.shape != q.shape or out.dtype not in _OUT_DTYPES or not _rows_in_one_piece(out):
         raise ValueError("out must be [B][T][Hq][D] with contiguous rows")
     else:
         os_ = _row_strides(out)

@@ -162,3 +162,25 @@ def test_a_workspace_that_is_not_one_piece_is_refused():
         c.run(plan=plan, workspace=torch.zeros(n - 1, dtype=torch.uint8, device=dev))
     want, bound = c.want()
     _attend_close(c.run(plan=plan, workspace=torch.zeros(n // 4 + 1, dtype=torch.float32, device=dev)), want, bound)
+
+
+@pytest.mark.parametrize("T", [1, 6])
+def test_one_head_out_of_a_transposed_layout(T):
+    # [B][H][T][D] transposed: with one head, rows are in one piece whatever that axis's stride is;
+    # keys and values of one sequence or token may differ in the strides of those axes
+    dev = cuda()
+    g = torch.Generator(device=dev).manual_seed(T)
+    q, k, v = (torch.randn(1, 1, T, 128, generator=g, device=dev).half() for _ in "qkv")
+    v = torch.cat((v, v), 0)[:1] if T > 1 else torch.cat((v, v), 2)[:, :, :1]
+    ro = q4.Rotary(q4.Rotary.make_table(10000.0 ** (-torch.arange(64) / 64), 60, device=dev))
+    tab, lens = torch.tensor([[1, 0]], device=dev), torch.tensor([20], device=dev)
+    outs = []
+    for turn in (lambda x: x.transpose(1, 2), lambda x: x.transpose(1, 2).contiguous()):
+        pool = q4.Q4KVPool(1, 128, 2, device=dev)
+        qr = pool.append_rotary(turn(k), turn(v), ro, tab, lens, q=turn(q), q_out=turn(torch.empty_like(q)))
+        o = q4.extend_attention(pool, qr, tab, lens, out=turn(torch.empty(1, 1, T, 128, device=dev)))
+        kv = torch.empty(2, 1, T, 128, dtype=torch.float16, device=dev)
+        kk, vv = pool.gather(tab, lens, torch.tensor([0, T], device=dev), T, k_out=kv[0].transpose(0, 1), v_out=kv[1].transpose(0, 1))
+        assert pool.read_device_error() == 0 and torch.count_nonzero(vv) > 0
+        outs.append((qr, o, kk.clone(), vv.clone(), pool.k_codes4, pool.v_codes4))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
