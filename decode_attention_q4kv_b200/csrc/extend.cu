@@ -55,7 +55,8 @@ namespace {
 
 constexpr int kDecodeWarp0 = 16, kMmaWarp = 24, kFeedWarp = 25;
 constexpr int kThreads = 28 * 32;
-// Registers: 72 a thread at launch, shared out anew by role.
+// Registers: 72 a thread at launch (asked for with __maxnreg__; the launch looks, for
+// shares above what the block has would wait forever), shared out anew by role.
 constexpr int kRegs = 72, kOtherRegs = 56;
 constexpr float kNone = -3.0e38f; // reference maximum of a row that has seen nothing: below every logit
 constexpr int kCols = 64;        // logit columns of a softmax step
@@ -423,7 +424,7 @@ __device__ __forceinline__ Item item_of(const ExtendArgs& a) {
 }
 
 template <int MODE, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ ExtendArgs a, uint32_t raw_stride,
+__global__ void __maxnreg__(kRegs) extend_kernel(const __grid_constant__ ExtendArgs a, uint32_t raw_stride,
                                                              int n_raw) {
   using G = Geo<MODE>;
   constexpr int D = G::D, BN = G::BN;
