@@ -15,14 +15,18 @@
 // head and come as 8 shuffles of the raw 16-bit words.
 //
 // Bound by latency: each item looks up its length, block, positions and angles
-// before it can turn a row, and the 32 registers of angles beside the encoder's
-// leave room for 16 warps per SM with heads of 256.  8191 tokens of 16 query and
-// 8 KV heads of 256, bf16, take 80 us, 2.8 TB/s of the 220 MB that have to move
-// (34 us at the copy bandwidth; issue 43 %, 22 % of the warps resident).  With a
-// read-back of the chunk behind it, blocks of 256 threads at 3 per SM, which
-// spill, took 116 instead of 109 us there, but 62.5 instead of 68.6 us for
-// 4 x 2048 tokens of 32 and 8 heads of 128 on three axes, so only heads of 128
-// ask for 3.  Keys and values loaded before the look-ups: 132 us (155 registers).
+// before it can turn a row.  A half-pair lane holds 16 (cos, sin), 32 registers
+// beside the encoder's; an interleaved one 8.  So interleaved pairs ask for 3
+// blocks of 256 threads per SM and half pairs for 2 (at 3 they spill 356 and 564
+// bytes with heads of 128).  Measured, L2 flushed before each call, us at 2 / at 3 blocks:
+//   4 x 2048 tokens, 32/8 heads of 128, fp16     half 65.6 / 73.7   interleaved 59.4 / 56.3
+//   the same on three axes                       half 73.8 / 82.9   interleaved 67.6 / 63.6
+//   1 x 8191 tokens, 16/8 heads of 256, bf16     half 82.5 / 92.7   interleaved 77.8 / 73.7
+//   4 x 512 tokens, 32/8 heads of 128, fp16      half 26.7 / 35.7   interleaved 22.7 / 26.6
+// (of interleaved pairs the last goes the other way).
+// 8-bit, 2-bit and raw-key blocks and bf16 take the same within 3 %, E4M3 59.5.
+// 1 x 8191 moves 220 MB at 2.7 TB/s (34 us at the copy bandwidth; issue 43 %, 22 % of
+// the warps resident).  Keys and values loaded before the look-ups: 132 us (155 registers).
 #include "encode.cuh"
 #include "extend_internal.cuh"
 
@@ -85,7 +89,7 @@ __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[8]) {
 }
 
 template <int D, typename InT, bool ROT, bool INTER>
-__global__ void __launch_bounds__(256, D == 128 ? 3 : 2) append_rotary_kernel(const __grid_constant__ RotaryAppendArgs a, int per) {
+__global__ void __launch_bounds__(256, INTER ? 3 : 2) append_rotary_kernel(const __grid_constant__ RotaryAppendArgs a, int per) {
   using S = Shape<D>;
   griddep_wait();
   griddep_launch_dependents();
