@@ -25,12 +25,16 @@
 // subtraction per pair of codes leave); q is stored in the same order and the
 // output's columns are put back when they are written.
 //
-// Roundings: K and V to fp16 (one fused multiply-add code * s + z), q to fp16
-// after a power-of-two scaling per row, the weights to fp16 (scaled by 2^6, so
-// that weights down to 2^-30 of the largest survive); each is at most 2^-11
-// relative.  Maxima, sums and accumulators are binary32.  The running maximum
-// is only moved when it grows by more than 2^8: until then weights above 1 are
-// harmless (at most 2^14 in fp16), and the accumulator is not rescaled.
+// Roundings: K and V to fp16 (one fused multiply-add code * s + z), q (with scale
+// and log2(e) in it) to fp16 after a power-of-two scaling per row, the weights to
+// fp16 (scaled by 2^6, so that weights down to 2^-30 of the largest survive).  Each
+// is at most 2^-11 of what is rounded, or half a step of fp16's smallest numbers:
+// 2^-25 for K and V below 2^-14, 2^-31 of its row's largest channel for q, 2^-30 of
+// the row's largest weight for the weights.  Maxima, sums and accumulators are
+// binary32; the tensor cores cut off what they add up, up to 2^-12 of a sum over
+// the most tokens that a plan gives an accumulator.  The running maximum is only
+// moved when it grows by more than 2^8: until then weights above 1 are harmless (at
+// most 2^14 in fp16), and the accumulator is not rescaled.
 // For N(0, 1) inputs the output is off by 4e-4 of its size, 2e-4 of it the fp16
 // output's own rounding; codes are 4 bits, so the cache itself is off by percents.
 //
@@ -93,7 +97,7 @@ struct Geo {
   static constexpr int R = 128 * QT;
   static constexpr uint32_t kQ = QT * 128 * D * 2;
   static constexpr uint32_t kRawAt = kQ + kSlots * kTile;
-  static constexpr uint32_t kRawRing = ALT ? 65600 : 32800;   // 2 packed tiles of 8-bit codes, or 3 of 4-bit ones
+  static constexpr uint32_t kRawRing = ALT ? 65600 : 32800;   // 4 or 2 packed tiles of 8-bit codes, 7 or 3 of 4-bit ones
   static constexpr uint32_t kMiscAt = kRawAt + kRawRing;
 };
 
@@ -116,8 +120,10 @@ struct Misc {
   // (2^28 blocks of one width would be terabytes.)
   uint32_t raw_what[kMaxRaw];
   // Remapped slots of key tile j and whether its block id is out of range, at
-  // j % 8, from the key decoders to the softmax.  (When tile j + 8 is decoded,
-  // the keys of tile j + 6 are used up, and the softmax is past tile j.)
+  // j % 8, from the key decoders to the softmax.  (A decoder that writes for tile
+  // j + 8 has seen the keys of tile j + 5 used up.  Their products were issued after
+  // those of tile j + 3's values, which wait for that tile's weights, so the softmax
+  // is past tile j.)
   alignas(16) uint32_t gone[8][4];
   int bad[8];
   int odd_first, odd_last; // tokens of this CTA whose value is not finite lie between these

@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(256, 4) gather_kernel(const __grid_constant__ 
   const bool turn = a.unrotate_k && pool.k_rotated;
   const int64_t at = n * a.out_stride + j * kEPL;
   const int h1 = min(hkv, (part + 1) * per);
-  // the widths of a warp's rows differ only where a block ends among them
+  // The widths of a warp's rows differ only where a block ends among them.  Rows of
+  // 2-bit blocks take that way too: three walks over the heads, of which one loads.
   const bool all4 = __all_sync(0xffffffffu, bits == 4), all8 = __all_sync(0xffffffffu, bits == 8);
   const int h0 = part * per;
   OutT* kd = static_cast<OutT*>(a.k_out) + at + static_cast<int64_t>(h0) * D;

@@ -137,7 +137,8 @@ q4kv_status q4kv_extend_plan_make(int32_t batch, int32_t max_new, int32_t n_q_he
  *   block_tables device int32 [batch][max_blocks_per_seq]
  *   out          as q, of out_dtype (F32, F16 or BF16), its own strides; no
  *                two of its rows may share memory, nor may it overlap q
- *   softmax_scale <= 0 selects 1/sqrt(D)
+ *   softmax_scale <= 0 selects 1/sqrt(D); the scaled queries and the logits
+ *                have to be finite in binary32
  *   workspace    as for q4kv_decode_attention
  * Token i of sequence b sees the positions t <= seq_lens[b] + i and, with
  * plan->window > 0, t > seq_lens[b] + i - window.  Remapped slots have logit
