@@ -184,3 +184,34 @@ def test_one_head_out_of_a_transposed_layout(T):
         assert pool.read_device_error() == 0 and torch.count_nonzero(vv) > 0
         outs.append((qr, o, kk.clone(), vv.clone(), pool.k_codes4, pool.v_codes4))
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("T,hq,hkv,d,splits", [(70, 8, 2, 128, 0), (20, 8, 2, 128, 3), (4, 8, 2, 128, 0), (33, 4, 2, 256, 2)])
+def test_results_repeat_bit_for_bit_beside_other_work(T, hq, hkv, d, splits):
+    dev = cuda()
+    c = Case([1500, 2900, 40], T, hq, hkv, d, "bf16", n_new=[T, T - 1, T], widths=(4, 8), seed=T, kscale=6.0)
+    args = (c.pool, c.q.to(dev), c.dev(c.tables), c.dev(c.lens), c.dev(c.n_new))
+    plan = q4.ExtendPlan(3, T, hq, hkv, d, c.tables.shape[1], n_splits=splits)
+    first = q4.extend_attention(*args, plan=plan, out_dtype=torch.float32)
+    other, big = torch.cuda.Stream(), torch.zeros(1 << 26, device=dev)
+    torch.cuda.synchronize()
+    for i in range(40):
+        if i % 3:
+            with torch.cuda.stream(other):
+                big.add_(1.0)
+        assert torch.equal(q4.extend_attention(*args, plan=plan, out_dtype=torch.float32), first)
+    torch.cuda.synchronize()
+
+
+def test_a_padded_batch_of_prompts_sharing_their_first_blocks():
+    # two sequences over the same prefix blocks, an empty one, and one without new tokens
+    dev = cuda()
+    c = Case([512, 512, 0, 300], 30, 8, 2, 128, "fp16", n_new=[30, 11, 0, 0], seed=7)
+    c.tables[1][:2] = c.tables[0][:2]
+    want, bound = c.want()
+    out = torch.full((4, 30, 8, 128), 3.0, device=dev)
+    _attend_close(c.run(out=out), want, bound)
+    assert torch.count_nonzero(out[2:]) == 0 and torch.count_nonzero(out[1, 11:]) == 0
+    k, v = c.pool.gather(c.dev(c.tables), c.dev([0, 0, 0, 0]), c.dev([0, 512, 1024, 1024, 1324]), 1324)
+    assert torch.equal(k[:512], k[512:1024]) and torch.equal(v[:512], v[512:1024])
+    assert c.pool.read_device_error() == 0
