@@ -39,11 +39,13 @@
 // output's own rounding; codes are 4 bits, so the cache itself is off by percents.
 //
 // Bound by the softmax warps: a step of 128 tokens x 256 rows takes ~4200 cycles,
-// the products of it ~2050, and the CTA has 27000 cycles of start and end.  One
-// chunk of 512 tokens, 32/8 heads of 128, on 8192: 107 us, 0.39 of the measured
-// bf16 rate; issue 61 %, tensor pipe 42 %, exponentials' unit 44 %, no pipe full.
-// 2048 tokens on 32768 (a quarter of the blocks 8-bit): 1213 us (0.56).  Of 1165 us
-// (before values were checked) 770 were left without the softmax, 1028 without
+// the products of it ~2050, and the CTA has 27000 cycles of start and end (the plan's
+// fit; what they consist of was not taken apart).  One chunk of 512 tokens, 32/8 heads
+// of 128, on 8192: 107 us, 0.39 of the measured bf16 rate; issue 61 %, tensor pipe
+// 41 %, exponentials' unit 44 %, no pipe full.  2048 tokens on 32768 (a quarter of the
+// blocks 8-bit): 1157 us for a call by itself, 1374 in runs of minutes under the power
+// cap (0.58 and 0.49).  Of 1165 us of an earlier state of the kernel, without the looks for
+// what is not finite, 770 were left without the softmax, 1028 without
 // decoding, 1039 without the exponentials, 1145 with a sixteenth of the products.
 // Four softmax warps a row tile and parity hide the latency of tensor-memory loads
 // (~300 cycles while products run); polynomial exponentials on the FMA pipe, sleeping
@@ -79,14 +81,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 // MODE 3: MODE 1 for up to 32 rows: the tile holds each four times, and each copy
 //         takes 16 of a step's 64 columns (its weights of the others are 0), so
 //         that all four warps of a group have work; the copies are added up at
-//         the end.  16 x 5 tokens on up to 32768, 32/8 heads: 327 -> 279 us.
+//         the end.  MODE 1 / MODE 3, us, 32/8 heads: 16 x 5 tokens on up to 32768
+//         282 / 247, a quarter 8-bit 412 / 367, E4M3 488 / 446; 64 x 1 on 8192 386 / 335;
+//         8 x 8 on 8192 62.5 / 58.4; 1 x 4 on 32768 44 / 41; 4 x 30, 8/8 heads, on 16384
+//         64.5 / 58.4.  Heads of 256 have no such shape: up to 32 rows leave three of
+//         the four warps of a group without work there.
 template <int MODE>
 struct Geo {
   static constexpr bool ALT = MODE == 1 || MODE == 3;  // alternate key tiles
   static constexpr int COPIES = MODE == 3 ? 4 : 1;     // of a row in the tile
   // Registers of a softmax and of a decoding thread.  With 16 columns a thread the
   // softmax needs fewer, and a lane can decode its four tokens at once
-  // (16 x 5 tokens on up to 32768: 297 -> 279 us).
+  // (the calls above with the shares and lanes of the other shapes: 267, 397, 451,
+  // 360, 60.4, 42 and 62.3 us).
   static constexpr int kSoftRegs = MODE == 3 ? 64 : 88, kDecodeRegs = MODE == 3 ? 96 : 48, kAtOnce = MODE == 3 ? 4 : 1;
   static_assert(16 * kSoftRegs + 8 * kDecodeRegs + 4 * kOtherRegs <= 28 * kRegs, "register shares");
   static constexpr int D = MODE == 2 ? 256 : 128;
@@ -346,9 +353,11 @@ __device__ __forceinline__ void decode_tile(const uint8_t* raw, const uint8_t* p
 //
 // Whether one of the warp's tokens needs it is found out with one look at their
 // scales, two groups a lane.  Scales in shared memory are put right there, 8-bit
-// ones are left to decode_tile.  (Beside every token's decoding the check cost 8
-// to 13 % of whole calls, in a warp of its own, which delays the decoders, 1 to
-// 16 %; here 1 to 4 %, and 7 % for E4M3, whose bytes are looked at themselves.)
+// ones are left to decode_tile.  (Without any look 64 x 1 tokens on 8192 take 322 us
+// instead of 335, 16 x 5 on up to 32768 237 instead of 247, 4 x 509 on 16384 840
+// instead of 854, 5 x 256 with heads of 256 308 instead of 328, E4M3 of heads of 256
+// 172 instead of 178.  Beside every token's decoding the look at values alone cost 8 to
+// 13 %, in a warp of its own, which delays the decoders, 1 to 16 %.)
 template <int D, int MAX>
 __device__ __noinline__ void mend_groups(uint2* at, uint2 sz, bool key, bool live, int t, Misc* ms) {
   const bool fx = tame_group<MAX>(sz.x), fy = tame_group<MAX>(sz.y);
@@ -1121,7 +1130,7 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t stream) {
   if (a.pool.fp8) {
     if (p.head_dim == 256) return launch_mode<2, true>(a, stream);
     if (sh.rows == 256) return launch_mode<0, true>(a, stream);
-  return group_rows <= 32 ? launch_mode<3, true>(a, stream) : launch_mode<1, true>(a, stream);
+    return group_rows <= 32 ? launch_mode<3, true>(a, stream) : launch_mode<1, true>(a, stream);
   }
   if (p.head_dim == 256) return launch_mode<2, false>(a, stream);
   if (sh.rows == 256) return launch_mode<0, false>(a, stream);

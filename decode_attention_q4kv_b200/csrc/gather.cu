@@ -13,10 +13,10 @@
 // of the rate.
 //
 // Bound by memory: 10 x 32768 tokens of 8 heads of 128, a quarter of the blocks
-// 8-bit, to fp16 with the keys un-rotated take 322 us, 5.6 TB/s of the 1.8 GB that
-// have to move (0.87 of the copy bandwidth).  With one head per look-up and
-// integer conversions it was 483 us; without the codes of the next head on
-// their way 404 us; at 3 blocks per SM instead of 4, 348 us.
+// 8-bit, to fp16 with the keys un-rotated take 350 us, 5.1 TB/s of the 1.8 GB that
+// have to move (0.80 of the copy bandwidth; 322 us, 0.87, in a short run).  In short
+// runs it was 483 us with one head per look-up and integer conversions, 404 us
+// without the codes of the next head on their way, 348 us at 3 blocks per SM instead of 4.
 #include "encode.cuh"
 #include "extend_internal.cuh"
 
