@@ -163,8 +163,8 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<co
 // Bounded wait.  When it runs out, abort is set and this and every later wait of
 // the block returns at once: the roles walk their loops to the end (every access
 // stays inside its buffers whatever they hold), the block waits for what is still
-// in flight, the rows are written as 0 and the error bit is raised.  No sleep between tries: every wait here is short and
-// on the critical path of the next role.
+// in flight, the rows are written as 0 and the error bit is raised.  No sleep
+// between tries: every wait here is short and on the critical path of the next role.
 struct Gate {
   Misc* ms;
   unsigned tries;          // of one wait
@@ -440,7 +440,7 @@ __device__ __forceinline__ Item item_of(const ExtendArgs& a) {
 
 template <int MODE, bool FP8>
 __global__ void __maxnreg__(kRegs) extend_kernel(const __grid_constant__ ExtendArgs a, uint32_t raw_stride,
-                                                             int n_raw) {
+                                                 int n_raw) {
   using G = Geo<MODE>;
   constexpr int D = G::D, BN = G::BN;
   extern __shared__ __align__(1024) uint8_t sm[];
